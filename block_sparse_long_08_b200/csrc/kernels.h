@@ -208,6 +208,57 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t st);
 cudaError_t launch_quantize_e4m3_rows(const uint16_t *x, long long rows, int cols, uint8_t *codes,
                                       float *scale, cudaStream_t st);
 
+// Dense attention over paged caches (paged_kernels.cu).
+struct PagedCache {
+  void *k, *v;                 // [num_pages, page, G, d] bf16, or E4M3 codes with scales
+  float *k_scale, *v_scale;    // null, or [num_pages, page, G]
+  const int32_t *table;        // [B, max_pages]
+  int num_pages, max_pages;
+  int page_log2;               // page size = 1 << page_log2
+};
+struct AppendArgs {
+  int B, Lmax, H, G, n_rows;   // H = 0: no queries
+  PagedCache c;
+  const uint16_t *q, *k, *v;   // [n_rows, H|G, d]
+  const int32_t *cu;           // [B+1] or null: one row per sequence
+  const int32_t *seq_lens;     // [B], new tokens included
+  const float *inv_freq;       // [rot/2]
+  int rot, interleaved;
+  uint16_t *q_out, *k_out;     // null: not written
+  int *status;
+};
+cudaError_t launch_paged_append(const AppendArgs &a, int num_sms, cudaStream_t st);
+
+struct PagedDecodeArgs {
+  int B, Lmax, H, G;
+  PagedCache c;
+  float scale, scale_log2;
+  const uint16_t *q;           // [B,H,d]
+  const int32_t *seq_lens;     // [B]
+  uint16_t *out;               // [B,H,d]
+  float *lse;                  // [B,H] or null
+  int *status;
+};
+cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int num_sms, cudaStream_t st);
+
+// Dense attention over packed sequences (dense_kernels.cu).  The plan kernel
+// checks cu_q and cu_k and writes each sequence's {q0, nq, k0, nk} (all zero
+// when the batch is refused).
+struct DenseArgs {
+  int B, H, G, nq, nk;
+  float scale, scale_log2;
+  const uint16_t *q, *k, *v;   // packed rows [nq,H,d], [nk,G,d]
+  const int32_t *cu_q, *cu_k;  // [B+1]
+  int4 *seqs;                  // [B]
+  uint16_t *out;               // [nq,H,d] (read by the backward)
+  float *lse;                  // [nq,H] or null
+  const uint16_t *dout;        // backward
+  uint16_t *dq, *dk, *dv;
+  int *status;
+};
+cudaError_t launch_dense_varlen(const DenseArgs &a, int num_sms, cudaStream_t st);
+cudaError_t launch_dense_varlen_backward(const DenseArgs &a, int num_sms, cudaStream_t st);
+
 // Sets the message msa_last_error() returns; returns `code`.
 int report_error(int code, const char *msg);
 

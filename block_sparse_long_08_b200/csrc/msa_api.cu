@@ -630,6 +630,96 @@ int nsa_gate(const msa_params *p, const float *gates, const msa_bf16 *o_cmp, con
   return MSA_OK;
 }
 
+// ---- dense attention over paged caches and packed sequences -------------------
+int check_dense_params(const msa_params *p) {
+  if (!p) return fail(MSA_ERR_INVALID_ARG, "params is NULL");
+  if (p->B < 0 || p->L < 0 || p->H <= 0 || p->G <= 0 || p->d <= 0)
+    return fail(MSA_ERR_INVALID_ARG, "negative or zero size in params");
+  if (!std::isfinite(p->scale) || p->scale < 0.f)
+    return fail(MSA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (p->d != 128) return fail(MSA_ERR_UNSUPPORTED, "d=%d (supported: 128)", p->d);
+  if (p->H % p->G != 0) return fail(MSA_ERR_INVALID_ARG, "H=%d not a multiple of G=%d", p->H, p->G);
+  const int r = p->H / p->G;
+  if (r != 1 && r != 2 && r != 4 && r != 8 && r != 16)
+    return fail(MSA_ERR_UNSUPPORTED, "H/G=%d (supported: 1,2,4,8,16)", r);
+  if (p->H > 1024) return fail(MSA_ERR_UNSUPPORTED, "H=%d above 1024", p->H);
+  if (p->B > (1 << 20)) return fail(MSA_ERR_UNSUPPORTED, "B=%d above 2^20", p->B);
+  if (p->L > (1 << 26)) return fail(MSA_ERR_UNSUPPORTED, "L=%d above 2^26", p->L);
+  return MSA_OK;
+}
+
+bool dense_op(int op) { return op >= MSA_OP_PAGED_APPEND && op <= MSA_OP_DENSE_VARLEN_BACKWARD; }
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Packed-sequence operations: {q0, nq, k0, nk} per sequence.
+struct DenseWs {
+  size_t seqs, end;
+};
+DenseWs dense_ws(const msa_params *p) {
+  DenseWs w;
+  size_t o = msa::kWsHeader;
+  w.seqs = o; o = align_up(o + sizeof(int4) * size_t(p->B));
+  w.end = o;
+  return w;
+}
+
+size_t dense_ws_bytes(const msa_params *p, int op) {
+  if (op == MSA_OP_DENSE_VARLEN || op == MSA_OP_DENSE_VARLEN_BACKWARD) return dense_ws(p).end;
+  return msa::kWsHeader;
+}
+
+int check_cache(const msa_params *p, const msa_paged_cache *c, msa::PagedCache *out) {
+  if (!c) return fail(MSA_ERR_INVALID_ARG, "cache is NULL");
+  int lg = 4;
+  while (lg <= 8 && (1 << lg) != c->page_size) ++lg;
+  if (lg > 8)
+    return fail(MSA_ERR_UNSUPPORTED, "page_size=%d (supported: 16, 32, 64, 128, 256)", c->page_size);
+  if (c->num_pages < 0 || c->max_pages < 0)
+    return fail(MSA_ERR_INVALID_ARG, "negative num_pages or max_pages");
+  if ((long long)c->max_pages * c->page_size < p->L)
+    return fail(MSA_ERR_INVALID_ARG, "L=%d above max_pages * page_size = %lld", p->L,
+                (long long)c->max_pages * c->page_size);
+  if (!c->k || !c->v || !c->page_table) return fail(MSA_ERR_INVALID_ARG, "NULL cache pointer");
+  if ((c->k_scale == nullptr) != (c->v_scale == nullptr))
+    return fail(MSA_ERR_INVALID_ARG, "an 8-bit cache needs both k_scale and v_scale");
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->page_table) || !aligned4(c->k_scale) ||
+      !aligned4(c->v_scale))
+    return fail(MSA_ERR_INVALID_ARG, "cache pages must be 16-byte aligned (scales, table 4-byte)");
+  out->k = c->k; out->v = c->v;
+  out->k_scale = c->k_scale; out->v_scale = c->v_scale;
+  out->table = c->page_table;
+  out->num_pages = c->num_pages; out->max_pages = c->max_pages;
+  out->page_log2 = lg;
+  return MSA_OK;
+}
+
+// Checks and arguments shared by the packed-sequence forward and backward.
+int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa_bf16 *k,
+               const msa_bf16 *v, const int32_t *cu_q, const int32_t *cu_k, const void *out,
+               const float *lse, void *ws, size_t ws_bytes, msa::DenseArgs *a) {
+  if (nq < 0 || nk < 0 || nq > p->L || nk > p->L)
+    return fail(MSA_ERR_INVALID_ARG, "nq=%d nk=%d: need 0 <= nq, nk <= L=%d", nq, nk, p->L);
+  if (!cu_q || !cu_k || (nq > 0 && (!q || !out)) || (nk > 0 && (!k || !v)))
+    return fail(MSA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned4(cu_q) ||
+      !aligned4(cu_k) || !aligned4(lse))
+    return fail(MSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned (cu, lse 4-byte)");
+  const DenseWs w = dense_ws(p);
+  const int rc = check_ws(ws, ws_bytes, w.end);
+  if (rc) return rc;
+  a->B = p->B; a->H = p->H; a->G = p->G; a->nq = nq; a->nk = nk;
+  a->scale = eff_scale(p);
+  a->scale_log2 = a->scale * 1.4426950408889634f;
+  a->q = q; a->k = k; a->v = v;
+  a->cu_q = cu_q; a->cu_k = cu_k;
+  a->seqs = reinterpret_cast<int4 *>(reinterpret_cast<uint8_t *>(ws) + w.seqs);
+  a->out = nullptr; a->lse = nullptr;
+  a->dout = nullptr; a->dq = a->dk = a->dv = nullptr;
+  a->status = status_ptr(ws);
+  return MSA_OK;
+}
+
 }  // namespace
 
 namespace msa {
@@ -669,6 +759,7 @@ const char *msa_version(void) { return "msa-b200 0.1 (sm_100a)"; }
 
 size_t msa_workspace_bytes(const msa_params *p, int op) {
   g_err[0] = 0;
+  if (dense_op(op)) return check_dense_params(p) == MSA_OK ? dense_ws_bytes(p, op) : 0;
   if (check_params(p, op == MSA_OP_DECODE) != MSA_OK) return 0;
   switch (op) {
     case MSA_OP_INDEX_SELECT: return msa::kWsHeader;
@@ -1188,6 +1279,115 @@ int msa_nsa_forward(const msa_params *p, int32_t window, const msa_bf16 *q, cons
   rc = run_dense(p, 0, window, q, k, v, p->L, o_win, nullptr, ws, st);
   if (rc) return rc;
   return nsa_gate(p, gates, o_cmp, out, o_win, out, st);
+}
+
+int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, const msa_bf16 *q,
+                     const msa_bf16 *k, const msa_bf16 *v, const int32_t *cu_new,
+                     const int32_t *seq_lens, const float *inv_freq, int rot_dim, int interleaved,
+                     msa_bf16 *q_out, msa_bf16 *k_out, void *ws, size_t ws_bytes,
+                     msa_stream stream) {
+  g_err[0] = 0;
+  int rc = check_dense_params(p);
+  if (rc) return rc;
+  if (n_rows < 0) return fail(MSA_ERR_INVALID_ARG, "n_rows=%d", n_rows);
+  if (!cu_new && n_rows != p->B)
+    return fail(MSA_ERR_INVALID_ARG, "n_rows=%d without cu_new (B=%d)", n_rows, p->B);
+  if (rot_dim < 0 || rot_dim > p->d || rot_dim % 16 != 0)
+    return fail(MSA_ERR_UNSUPPORTED, "rot_dim=%d (supported: 0, 16, 32, ..., 128)", rot_dim);
+  if (p->B == 0 || n_rows == 0) return MSA_OK;
+  msa::AppendArgs a;
+  rc = check_cache(p, c, &a.c);
+  if (rc) return rc;
+  if (!k || !v || !seq_lens || (rot_dim > 0 && !inv_freq))
+    return fail(MSA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if ((q == nullptr) != (q_out == nullptr))
+    return fail(MSA_ERR_INVALID_ARG, "q and q_out go together");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned4(cu_new) || !aligned4(seq_lens) || !aligned4(inv_freq))
+    return fail(MSA_ERR_INVALID_ARG,
+                "tensor pointers must be 16-byte aligned (cu_new, seq_lens, inv_freq 4-byte)");
+  rc = check_ws(ws, ws_bytes, msa::kWsHeader);
+  if (rc) return rc;
+  a.B = p->B; a.Lmax = p->L; a.H = q ? p->H : 0; a.G = p->G; a.n_rows = n_rows;
+  a.q = q; a.k = k; a.v = v;
+  a.cu = cu_new; a.seq_lens = seq_lens;
+  a.inv_freq = inv_freq; a.rot = rot_dim; a.interleaved = interleaved != 0;
+  a.q_out = q_out; a.k_out = k_out;
+  a.status = status_ptr(ws);
+  cudaError_t e = msa::launch_paged_append(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged append launch");
+  return MSA_OK;
+}
+
+int msa_paged_attn_decode(const msa_params *p, const msa_paged_cache *c, const msa_bf16 *q,
+                          const int32_t *seq_lens, msa_bf16 *out, float *lse, void *ws,
+                          size_t ws_bytes, msa_stream stream) {
+  g_err[0] = 0;
+  int rc = check_dense_params(p);
+  if (rc) return rc;
+  if (p->B == 0) return MSA_OK;
+  msa::PagedDecodeArgs a;
+  rc = check_cache(p, c, &a.c);
+  if (rc) return rc;
+  if (!q || !seq_lens || !out) return fail(MSA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(out) || !aligned4(seq_lens) || !aligned4(lse))
+    return fail(MSA_ERR_INVALID_ARG,
+                "tensor pointers must be 16-byte aligned (seq_lens, lse 4-byte)");
+  rc = check_ws(ws, ws_bytes, dense_ws_bytes(p, MSA_OP_PAGED_DECODE));
+  if (rc) return rc;
+  a.B = p->B; a.Lmax = p->L; a.H = p->H; a.G = p->G;
+  a.scale = eff_scale(p);
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.q = q; a.seq_lens = seq_lens; a.out = out; a.lse = lse;
+  a.status = status_ptr(ws);
+  cudaError_t e = msa::launch_paged_decode(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+  return MSA_OK;
+}
+
+int msa_dense_attn_varlen(const msa_params *p, int nq, int nk, const msa_bf16 *q,
+                          const msa_bf16 *k, const msa_bf16 *v, const int32_t *cu_q,
+                          const int32_t *cu_k, msa_bf16 *out, float *lse, void *ws,
+                          size_t ws_bytes, msa_stream stream) {
+  g_err[0] = 0;
+  int rc = check_dense_params(p);
+  if (rc) return rc;
+  if (p->B == 0) return MSA_OK;
+  msa::DenseArgs a;
+  rc = dense_args(p, nq, nk, q, k, v, cu_q, cu_k, out, lse, ws, ws_bytes, &a);
+  if (rc) return rc;
+  if (nq == 0) return MSA_OK;
+  a.out = out;
+  a.lse = lse;
+  cudaError_t e = msa::launch_dense_varlen(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dense attention launch");
+  return MSA_OK;
+}
+
+int msa_dense_attn_varlen_backward(const msa_params *p, int nq, int nk, const msa_bf16 *q,
+                                   const msa_bf16 *k, const msa_bf16 *v, const msa_bf16 *out,
+                                   const float *lse, const msa_bf16 *dout, const int32_t *cu_q,
+                                   const int32_t *cu_k, msa_bf16 *dq, msa_bf16 *dk, msa_bf16 *dv,
+                                   void *ws, size_t ws_bytes, msa_stream stream) {
+  g_err[0] = 0;
+  int rc = check_dense_params(p);
+  if (rc) return rc;
+  if (p->B == 0) return MSA_OK;
+  msa::DenseArgs a;
+  rc = dense_args(p, nq, nk, q, k, v, cu_q, cu_k, out, lse, ws, ws_bytes, &a);
+  if (rc) return rc;
+  if ((nq > 0 && (!lse || !dout || !dq)) || (nk > 0 && (!dk || !dv)))
+    return fail(MSA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return fail(MSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (nq == 0 && nk == 0) return MSA_OK;
+  a.out = const_cast<msa_bf16 *>(out);
+  a.lse = const_cast<float *>(lse);
+  a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv;
+  cudaError_t e =
+      msa::launch_dense_varlen_backward(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dense attention backward launch");
+  return MSA_OK;
 }
 
 }  // extern "C"

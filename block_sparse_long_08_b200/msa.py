@@ -40,6 +40,10 @@ MSA_OP_BACKWARD = 4
 MSA_OP_FORWARD_VARLEN = 5
 MSA_OP_NSA_BRANCH = 6
 MSA_OP_NSA_FORWARD = 7
+MSA_OP_PAGED_APPEND = 8
+MSA_OP_PAGED_DECODE = 9
+MSA_OP_DENSE_VARLEN = 10
+MSA_OP_DENSE_VARLEN_BACKWARD = 11
 
 
 class MSAError(RuntimeError):
@@ -59,6 +63,13 @@ class msa_staging(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("q_idx", ctypes.c_void_p), ("k_idx", ctypes.c_void_p), ("out", ctypes.c_void_p),
                 ("lse", ctypes.c_void_p)]
+
+
+class msa_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -100,6 +111,13 @@ def lib() -> ctypes.CDLL:
         L.msa_nsa_gate.argtypes = [pp, _P, _P, _P, _P, _P, _P]
         L.msa_nsa_forward.argtypes = [pp, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
                                       _P]
+        pc, ci = ctypes.POINTER(msa_paged_cache), ctypes.c_int
+        L.msa_paged_append.argtypes = [pp, pc, ci, _P, _P, _P, _P, _P, _P, ci, ci, _P, _P, _P, _SZ,
+                                       _P]
+        L.msa_paged_attn_decode.argtypes = [pp, pc, _P, _P, _P, _P, _P, _SZ, _P]
+        L.msa_dense_attn_varlen.argtypes = [pp, ci, ci, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.msa_dense_attn_varlen_backward.argtypes = [pp, ci, ci, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                     _P, _P, _P, _SZ, _P]
         L.msa_workspace_bytes.argtypes = [pp, ctypes.c_int]
         L.msa_workspace_bytes.restype = _SZ
         L.msa_read_status.argtypes = [_P, _P]
@@ -112,7 +130,9 @@ def lib() -> ctypes.CDLL:
                   "msa_sparse_attn_decode_fp8idx", "msa_quantize_e4m3_rows",
                   "msa_sparse_attn_decode_fp8", "msa_forward_cached_varlen",
                   "msa_sparse_attn_backward", "msa_nsa_compress_kv", "msa_nsa_window_attn",
-                  "msa_nsa_compressed_attn", "msa_nsa_gate", "msa_nsa_forward"):
+                  "msa_nsa_compressed_attn", "msa_nsa_gate", "msa_nsa_forward",
+                  "msa_paged_append", "msa_paged_attn_decode", "msa_dense_attn_varlen",
+                  "msa_dense_attn_varlen_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -704,6 +724,216 @@ def msa_sparse_attn_decode_noalloc(q, q_idx, k_cache, v_cache, k_idx_cache, seq_
                                                 _ptr(v_cache), _ptr(k_idx_cache), _ptr(seq_lens),
                                                 _ptr(out), _ptr(sel), _stream(stream)))
     return (out, sel) if want_sel else out
+
+
+# ---- dense attention over paged caches and packed sequences (see include/msa.h)
+
+def _one_device(dev, *named):
+    """Every tensor of a call lies on one device."""
+    for n, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, the call's tensors are on {dev}")
+
+
+class _on_device:
+    """The call's device as the current one: streams, launches and the SM
+    count the library asks for belong to the device of the tensors."""
+
+    def __init__(self, dev):
+        self.want = dev.index if dev.type == "cuda" else None
+
+    def __enter__(self):
+        self.back = None
+        if self.want is not None:
+            cur = torch.cuda.current_device()
+            if cur != self.want:
+                self.back = cur
+                torch.cuda.set_device(self.want)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def new_paged_workspace(op: int, page_table, page_size: int, H: int, G: int) -> torch.Tensor:
+    """Zeroed workspace of msa_paged_append or msa_paged_attn_decode."""
+    B, cols = page_table.shape
+    return new_workspace(make_params(B, cols * page_size, H, G), op, page_table.device)
+
+
+def new_dense_workspace(op: int, q, k, B: int) -> torch.Tensor:
+    """Zeroed workspace of msa_dense_attn_varlen or its backward: packed q
+    [nq,H,d], k [nk,G,d] of B sequences."""
+    return new_workspace(make_params(B, max(q.shape[0], k.shape[0]), q.shape[1], k.shape[1]), op,
+                         q.device)
+
+
+def _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G):
+    """The cache's checks: k_pages, v_pages [num_pages, page_size, G, d]."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or page_table.dim() != 2:
+        raise ValueError("k_pages, v_pages must be [num_pages, page_size, G, d], page_table [B, cols]")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("an 8-bit cache needs both k_scale and v_scale")
+    num, page, g, d = k_pages.shape
+    if g != G:
+        raise ValueError(f"the cache has {g} KV heads, the call {G}")
+    kind = torch.bfloat16 if k_scale is None else torch.uint8
+    _req(k_pages, "k_pages", kind)
+    _req(v_pages, "v_pages", kind)
+    _req(page_table, "page_table", torch.int32)
+    if k_scale is not None:
+        _size(k_scale, "k_scale", torch.float32, num * page * G)
+        _size(v_scale, "v_scale", torch.float32, num * page * G)
+    c = msa_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(),
+                        k_scale.data_ptr() if k_scale is not None else None,
+                        v_scale.data_ptr() if v_scale is not None else None,
+                        page_table.data_ptr(), num, page, page_table.shape[1])
+    return c, page_table.shape[0], page_table.shape[1] * page, d
+
+
+def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=None, q=None,
+                     q_out=None, k_out=None, inv_freq=None, rot_dim: Optional[int] = None,
+                     interleaved: bool = False, k_scale=None, v_scale=None, ws=None, stream=None):
+    """Append new tokens' k, v [N,G,d] to the paged cache (k_pages, v_pages
+    [num_pages,page_size,G,d] bf16, or uint8 E4M3 codes with k_scale, v_scale
+    [num_pages,page_size,G] fp32), the keys and q [N,H,d] rotated by position.
+    page_table [B,cols], seq_lens [B] (new tokens included), cu_new [B+1]
+    (None: one row per sequence), all int32.  rot_dim defaults to twice
+    inv_freq's length.  Returns q_out (allocated unless given; None without
+    q); k_out, when given, receives the rotated keys."""
+    N, G, d = k.shape
+    for n_, t in (("k", k), ("v", v)):
+        _size(t, n_, torch.bfloat16, N * G * d)
+    c, B, L, dc = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G)
+    if dc != d:
+        raise ValueError(f"the cache's head dim is {dc}, the keys' {d}")
+    _size(seq_lens, "seq_lens", torch.int32, B)
+    if cu_new is not None:
+        _size(cu_new, "cu_new", torch.int32, B + 1)
+    elif N != B:
+        raise ValueError(f"{N} rows for {B} sequences need cu_new")
+    if rot_dim is None:
+        rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot_dim:
+        if inv_freq is None:
+            raise ValueError("rot_dim needs inv_freq")
+        _size(inv_freq, "inv_freq", torch.float32, rot_dim // 2)
+    H = G
+    if q is not None:
+        H = q.shape[1]
+        _size(q, "q", torch.bfloat16, N * H * d)
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        _size(q_out, "q_out", torch.bfloat16, N * H * d)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None:
+        _size(k_out, "k_out", torch.bfloat16, N * G * d)
+    _one_device(k.device, ("v", v), ("k_pages", k_pages), ("v_pages", v_pages),
+                ("page_table", page_table), ("seq_lens", seq_lens), ("cu_new", cu_new), ("q", q),
+                ("q_out", q_out), ("k_out", k_out), ("inv_freq", inv_freq), ("k_scale", k_scale),
+                ("v_scale", v_scale), ("ws", ws))
+    p = make_params(B, L, H, G, d)
+    with _on_device(k.device):
+        ws = _ensure_ws(ws, p, MSA_OP_PAGED_APPEND, k.device)
+        _check(lib().msa_paged_append(ctypes.byref(p), ctypes.byref(c), N, _ptr(q), _ptr(k), _ptr(v),
+                                      _ptr(cu_new), _ptr(seq_lens), _ptr(inv_freq), int(rot_dim),
+                                      int(bool(interleaved)), _ptr(q_out), _ptr(k_out), _ptr(ws),
+                                      ws.numel(), _stream(stream)))
+    return q_out
+
+
+def msa_paged_attn_decode(q, k_pages, v_pages, page_table, seq_lens, *, k_scale=None, v_scale=None,
+                          scale: float = 0.0, want_lse: bool = False, out=None, lse=None, ws=None,
+                          stream=None):
+    """Dense attention of one new token per sequence, q [B,H,d], over the
+    first seq_lens[b] tokens of a paged cache (see msa_paged_append) ->
+    out [B,H,d] (and lse [B,H] when want_lse or given)."""
+    B, H, d = q.shape
+    _req(q, "q", torch.bfloat16)
+    G = k_pages.shape[2]
+    c, Bt, L, dc = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G)
+    if dc != d or Bt < B:
+        raise ValueError(f"cache head dim {dc}, page_table rows {Bt}: the call has {d} and {B}")
+    _size(seq_lens, "seq_lens", torch.int32, B)
+    out = torch.empty_like(q) if out is None else out
+    _size(out, "out", torch.bfloat16, B * H * d)
+    if lse is None and want_lse:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _size(lse, "lse", torch.float32, B * H)
+    _one_device(q.device, ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
+                ("seq_lens", seq_lens), ("k_scale", k_scale), ("v_scale", v_scale), ("out", out),
+                ("lse", lse), ("ws", ws))
+    p = make_params(B, L, H, G, d, scale=scale)
+    with _on_device(q.device):
+        ws = _ensure_ws(ws, p, MSA_OP_PAGED_DECODE, q.device)
+        _check(lib().msa_paged_attn_decode(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(seq_lens),
+                                           _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                           _stream(stream)))
+    return (out, lse) if lse is not None else out
+
+
+def _dense_inputs(q, k, v, cu_q, cu_k, scale):
+    nq, H, d = q.shape
+    nk, G = k.shape[0], k.shape[1]
+    _req(q, "q", torch.bfloat16)
+    for n_, t in (("k", k), ("v", v)):
+        _size(t, n_, torch.bfloat16, nk * G * d)
+    _req(cu_q, "cu_q", torch.int32)
+    B = cu_q.numel() - 1
+    if B < 0:
+        raise ValueError("cu_q needs one entry more than there are sequences")
+    _size(cu_k, "cu_k", torch.int32, B + 1)
+    return nq, nk, make_params(B, max(nq, nk), H, G, d, scale=scale)
+
+
+def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: bool = False,
+                          out=None, lse=None, ws=None, stream=None):
+    """Dense causal attention over packed sequences: q [nq,H,d], k, v
+    [nk,G,d], cu_q and cu_k [B+1] int32 (device), queries aligned to the end
+    of their sequence's keys -> out [nq,H,d] (and lse [nq,H] when want_lse or
+    given).  Rows behind cu_q[B] are left as they were."""
+    nq, nk, p = _dense_inputs(q, k, v, cu_q, cu_k, scale)
+    H, d = q.shape[1], q.shape[2]
+    out = torch.empty_like(q) if out is None else out
+    _size(out, "out", torch.bfloat16, nq * H * d)
+    if lse is None and want_lse:
+        lse = torch.empty((nq, H), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _size(lse, "lse", torch.float32, nq * H)
+    _one_device(q.device, ("k", k), ("v", v), ("cu_q", cu_q), ("cu_k", cu_k), ("out", out),
+                ("lse", lse), ("ws", ws))
+    with _on_device(q.device):
+        ws = _ensure_ws(ws, p, MSA_OP_DENSE_VARLEN, q.device)
+        _check(lib().msa_dense_attn_varlen(ctypes.byref(p), nq, nk, _ptr(q), _ptr(k), _ptr(v),
+                                           _ptr(cu_q), _ptr(cu_k), _ptr(out), _ptr(lse), _ptr(ws),
+                                           ws.numel(), _stream(stream)))
+    return (out, lse) if lse is not None else out
+
+
+def msa_dense_attn_varlen_backward(q, k, v, out, lse, dout, cu_q, cu_k, *, scale: float = 0.0,
+                                   dq=None, dk=None, dv=None, ws=None, stream=None):
+    """Gradients of msa_dense_attn_varlen: its inputs, its out [nq,H,d] and lse
+    [nq,H], dout [nq,H,d] -> (dq, dk, dv) bf16, shaped like q, k, v."""
+    nq, nk, p = _dense_inputs(q, k, v, cu_q, cu_k, scale)
+    H, d, G = q.shape[1], q.shape[2], k.shape[1]
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for n_, t in (("out", out), ("dout", dout), ("dq", dq)):
+        _size(t, n_, torch.bfloat16, nq * H * d)
+    for n_, t in (("dk", dk), ("dv", dv)):
+        _size(t, n_, torch.bfloat16, nk * G * d)
+    _size(lse, "lse", torch.float32, nq * H)
+    _one_device(q.device, ("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout),
+                ("cu_q", cu_q), ("cu_k", cu_k), ("dq", dq), ("dk", dk), ("dv", dv), ("ws", ws))
+    with _on_device(q.device):
+        ws = _ensure_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, q.device)
+        _check(lib().msa_dense_attn_varlen_backward(
+            ctypes.byref(p), nq, nk, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+            _ptr(cu_q), _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
+            _stream(stream)))
+    return dq, dk, dv
 
 
 def msa_read_status(ws: torch.Tensor, stream=None) -> int:

@@ -107,7 +107,11 @@ enum {
   MSA_OP_BACKWARD = 4,
   MSA_OP_FORWARD_VARLEN = 5,
   MSA_OP_NSA_BRANCH = 6,     /* msa_nsa_window_attn, msa_nsa_compressed_attn */
-  MSA_OP_NSA_FORWARD = 7     /* msa_nsa_forward */
+  MSA_OP_NSA_FORWARD = 7,    /* msa_nsa_forward */
+  MSA_OP_PAGED_APPEND = 8,   /* msa_paged_append */
+  MSA_OP_PAGED_DECODE = 9,   /* msa_paged_attn_decode */
+  MSA_OP_DENSE_VARLEN = 10,  /* msa_dense_attn_varlen */
+  MSA_OP_DENSE_VARLEN_BACKWARD = 11   /* msa_dense_attn_varlen_backward */
 };
 
 /* Index Branch (explainer §2.1; researchpapers.dev "机制").
@@ -399,6 +403,118 @@ int msa_nsa_forward(const msa_params *p, int32_t window, const msa_bf16 *q, cons
                     const msa_bf16 *v, const msa_bf16 *q_idx, const msa_bf16 *k_idx,
                     const float *gates, msa_bf16 *out, int32_t *sel, void *ws, size_t ws_bytes,
                     msa_stream stream);
+
+/* ---- Dense attention over paged caches and packed sequences ---------------
+ * The full-attention side of a model whose other layers are sparse (the
+ * explainer's §3.1 names a dense per-layer fallback, and a sparse model is
+ * warmed up on dense attention): exact causal attention over every key, with
+ * the same grouped heads, head dim and types as the sparse operations.
+ *   out[h] = sum_s P_s v[s,g],  P_s = exp(scale q[h].k[s,g] - lse[h]),
+ *   lse[h] = ln sum_s exp(scale q[h].k[s,g]),  g = h/(H/G),
+ *   s over the visible keys; a row that sees no key has out 0 and lse -inf.
+ * Of params these calls use B, L, H, G, d and scale (d == 128, H/G in
+ * {1,2,4,8,16}, B <= 2^20, L <= 2^26); d_idx, block, top_k and chunk are
+ * ignored, and neither G <= 8 nor B*L <= 2^26 is asked for.
+ *
+ * A paged cache.  Token t of sequence b lives in row t % page_size of page
+ * page_table[b][t / page_size], one table for keys and values. */
+typedef struct msa_paged_cache {
+  void *k, *v;                 /* [num_pages, page_size, G, d] bf16, or uint8
+                                  E4M3 codes when the scales are given     */
+  float *k_scale, *v_scale;    /* NULL, or [num_pages, page_size, G] fp32:
+                                  stored value = scale * E4M3(code)        */
+  const int32_t *page_table;   /* [B, max_pages] DEVICE array; entries
+                                  behind a sequence's last page are not read */
+  int32_t num_pages;
+  int32_t page_size;           /* 16, 32, 64, 128 or 256                   */
+  int32_t max_pages;           /* columns of page_table                    */
+} msa_paged_cache;
+
+/* Append the keys and values of new tokens to a paged cache, the keys (and
+ * queries) rotated by their position on the way.
+ *   p->B sequences; p->L: the most tokens a sequence may hold,
+ *     <= max_pages * page_size
+ *   k, v [n_rows, G, d] bf16: the new tokens' rows, packed               (in)
+ *   q [n_rows, H, d] bf16 or NULL; q_out [n_rows, H, d]: rotated queries
+ *     (q_out may be q; both or neither given)                        (in/out)
+ *   k_out [n_rows, G, d] bf16 or NULL: the rotated keys as bf16, for an
+ *     attention over the packed rows themselves (may be k)              (out)
+ *   cu_new [B+1] int32 DEVICE: sequence b owns rows [cu_new[b], cu_new[b+1]);
+ *     NULL: one row per sequence, n_rows == B                            (in)
+ *   seq_lens [B] int32 DEVICE: tokens of each sequence, the new ones
+ *     included: the i-th of n_b new rows is token seq_lens[b] - n_b + i.
+ *     0 marks a padding sequence: its rows are skipped                   (in)
+ *   inv_freq [rot_dim/2] fp32 DEVICE, NULL when rot_dim is 0             (in)
+ *   rot_dim: leading head dims that are rotated, 0 or a multiple of 16 up to
+ *     128; dims i and i + rot_dim/2 are a pair, or dims 2i and 2i + 1 when
+ *     `interleaved` is not 0.  A pair (x, y) at token t becomes
+ *     (x cos a - y sin a, y cos a + x sin a), a = t * inv_freq[i], the
+ *     product and its reduction in 64 bits, the rotation in fp32.
+ * An 8-bit cache gets scale = max|x| / 448 of the rotated fp32 row (1 for an
+ * all-zero row) and E4M3 round-to-nearest-even codes of x / scale.
+ * Rows at and behind cu_new[B], and cache rows that no new token owns, are
+ * left as they were.  A sequence with seq_lens[b] outside [n_b, p->L] or
+ * cu_new not ascending inside [0, n_rows], and a token whose page id lies
+ * outside [0, num_pages), are skipped and set MSA_ERR_DEVICE_INPUT.  Two new
+ * tokens that share a cache row are written in no particular order.
+ * ws >= msa_workspace_bytes(p, MSA_OP_PAGED_APPEND) (the status word). */
+int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, const msa_bf16 *q,
+                     const msa_bf16 *k, const msa_bf16 *v, const int32_t *cu_new,
+                     const int32_t *seq_lens, const float *inv_freq, int rot_dim, int interleaved,
+                     msa_bf16 *q_out, msa_bf16 *k_out, void *ws, size_t ws_bytes,
+                     msa_stream stream);
+
+/* Dense attention of one new token per sequence over a paged cache, the new
+ * token's key and value already appended.
+ *   q [B,H,d] bf16                                                       (in)
+ *   seq_lens [B] int32 DEVICE: cached tokens of each sequence, in [0, p->L];
+ *     0 (a padding sequence) gives out 0, lse -inf                       (in)
+ *   out [B,H,d] bf16; lse [B,H] fp32 or NULL                            (out)
+ * Cache rows at and behind seq_lens[b] may hold anything.  seq_lens[b]
+ * outside [0, p->L] sets MSA_ERR_DEVICE_INPUT (out 0, lse -inf); the keys of
+ * a page whose id lies outside [0, num_pages) are left out and set it too.
+ * The cache's tokens are shared out over the SMs whatever the lengths, the
+ * parts of one sequence joined by a second launch; the split depends on
+ * the lengths alone, so results repeat bit for bit.
+ * An 8-bit cache's scores run in f16 (|q| < 65504); each value's scale is
+ * folded into its softmax weight before the weight is rounded to bf16.
+ * ws >= msa_workspace_bytes(p, MSA_OP_PAGED_DECODE). */
+int msa_paged_attn_decode(const msa_params *p, const msa_paged_cache *c, const msa_bf16 *q,
+                          const int32_t *seq_lens, msa_bf16 *out, float *lse, void *ws,
+                          size_t ws_bytes, msa_stream stream);
+
+/* Dense causal attention over packed sequences of different lengths.
+ *   q [nq,H,d], k, v [nk,G,d] bf16: packed rows; nq, nk <= p->L          (in)
+ *   cu_q, cu_k [B+1] int32 DEVICE: sequence b owns query rows
+ *     [cu_q[b], cu_q[b+1]) and key rows [cu_k[b], cu_k[b+1]); either may be
+ *     empty.  Queries are aligned to the END of the keys: the i-th of n
+ *     query rows sees the first m - n + i + 1 of m keys (a cached prefix
+ *     when m > n; the first n - m rows see none when m < n)              (in)
+ *   out [nq,H,d] bf16; lse [nq,H] fp32 or NULL                          (out)
+ * Rows at and behind cu_q[B] are left as they were.  cu_q or cu_k not
+ * ascending inside [0, nq] or [0, nk] sets MSA_ERR_DEVICE_INPUT and nothing
+ * is written.  A sequence's own keys and values are finite; rows of other
+ * sequences and rows behind the last one may hold anything.
+ * ws >= msa_workspace_bytes(p, MSA_OP_DENSE_VARLEN). */
+int msa_dense_attn_varlen(const msa_params *p, int nq, int nk, const msa_bf16 *q,
+                          const msa_bf16 *k, const msa_bf16 *v, const int32_t *cu_q,
+                          const int32_t *cu_k, msa_bf16 *out, float *lse, void *ws,
+                          size_t ws_bytes, msa_stream stream);
+
+/* Backward pass of msa_dense_attn_varlen.
+ *   out, lse: the forward's outputs; dout [nq,H,d] bf16                  (in)
+ *   dq [nq,H,d], dk, dv [nk,G,d] bf16                                   (out)
+ * With dP_s = dout.v_s, D = dout.out, dZ_s = P_s (dP_s - D):
+ * dq = scale sum_s dZ_s k_s, dk_s += scale dZ_s q, dv_s += P_s dout over the
+ * rows and heads of the group that see s.  Keys no query sees, and queries
+ * that see no key, get zeros.  Rows behind cu_q[B] and cu_k[B] are left as
+ * they were; bit-identical from run to run.
+ * ws >= msa_workspace_bytes(p, MSA_OP_DENSE_VARLEN_BACKWARD). */
+int msa_dense_attn_varlen_backward(const msa_params *p, int nq, int nk, const msa_bf16 *q,
+                                   const msa_bf16 *k, const msa_bf16 *v, const msa_bf16 *out,
+                                   const float *lse, const msa_bf16 *dout, const int32_t *cu_q,
+                                   const int32_t *cu_k, msa_bf16 *dq, msa_bf16 *dk, msa_bf16 *dv,
+                                   void *ws, size_t ws_bytes, msa_stream stream);
 
 /* Workspace bytes op (MSA_OP_*) needs for these params; 0 when p is invalid
  * (see msa_last_error). */

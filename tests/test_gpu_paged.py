@@ -1,0 +1,296 @@
+"""Paged cache append and single-token attention on the GPU against the fp64
+oracle, whose tolerances are derived from the roundings (see dense_oracle).
+Append: one rounding to bf16 (or E4M3) of a value that is off by at most
+2^-20 of its pair's length (fp32 rotation by a cosine and sine good to 2^-22,
+two products and a sum).  L2 errors: independent roundings of at most 2^-8
+each have a root mean square of at most 2^-8 / sqrt(3) = 2.3e-3, so two of
+them (weights and output) stay below 3.2e-3; 4e-3 is asked for."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_long_08_b200.msa as M
+import oracle.dense_oracle as O
+from oracle.msa_oracle import e4m3_to_f64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16 = torch.bfloat16
+
+
+def f64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+def make_cache(lens, G, page, fp8, seed=0, extra=2, cols=None, junk=True):
+    """Scattered pages; every row of the pool that no token owns is NaN."""
+    gen = torch.Generator().manual_seed(seed)
+    need = [-(-max(n, 0) // page) for n in lens]
+    num = sum(need) + extra
+    ids = torch.randperm(num, generator=gen).to(torch.int32)
+    cols = cols or max(need + [1]) + 1
+    table = torch.full((len(lens), cols), -7, dtype=torch.int32)
+    own = torch.zeros(num, page, dtype=torch.bool)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        for t in range(max(lens[b], 0)):
+            own[table[b, t // page], t % page] = True
+        at += n
+    c = {"table": table.to(DEV), "own": own}
+    for x in "kv":
+        w = torch.randn(num, page, G, 128, generator=gen)
+        if fp8:
+            codes, scale = w.to(torch.float8_e4m3fn).view(torch.uint8), torch.rand(num, page, G, generator=gen) + 0.5
+            if junk:
+                codes[~own], scale[~own] = 0x7F, float("nan")
+            c[x], c[x + "s"] = codes.to(DEV), scale.to(DEV)
+        else:
+            w = w.to(BF16)
+            if junk:
+                w[~own] = float("nan")
+            c[x], c[x + "s"] = w.to(DEV), None
+    return c
+
+
+def cache_f64(c, x):
+    if c[x + "s"] is None:
+        return f64(c[x])
+    return e4m3_to_f64(c[x].cpu().numpy()) * f64(c[x + "s"])[..., None]
+
+
+def gathered(c, x, b, n):
+    w = cache_f64(c, x)
+    page = w.shape[1]
+    t = np.arange(n)
+    return w[c["table"].cpu().numpy()[b, t // page], t % page]
+
+
+def decode(c, q, lens, **kw):
+    t = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    return M.msa_paged_attn_decode(q, c["k"], c["v"], c["table"], t, k_scale=c["ks"], v_scale=c["vs"],
+                                   want_lse=True, **kw)
+
+
+def check_decode(c, q, lens, out, lse, scale=None, skip=None):
+    G = c["k"].shape[2]
+    B, H, d = q.shape
+    ref, tol = np.zeros(q.shape), np.zeros(q.shape)
+    for b, n in enumerate(lens):
+        k, v = gathered(c, "k", b, n), gathered(c, "v", b, n)
+        if skip is not None:
+            k, v = k[skip[b]], v[skip[b]]
+            n = k.shape[0]
+        o, ls, t, lt = O.dense(f64(q[b])[None], k, v, [0, 1], [0, n], scale)
+        ref[b], tol[b] = o[0], t[0]
+        got = f64(lse[b])
+        assert np.array_equal(np.isinf(got), np.isinf(ls[0])), b
+        fin = np.isfinite(got)
+        assert (np.abs(got[fin] - ls[0][fin]) <= lt[0][fin]).all(), (b, np.abs(got[fin] - ls[0][fin]).max())
+    err = np.abs(f64(out) - ref)
+    assert (err <= tol).all(), (err - tol).max()
+    assert np.linalg.norm(err) <= 4e-3 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G,R,page", [(2, 4, 64), (1, 16, 16), (8, 1, 32), (3, 2, 128), (2, 8, 256)])
+def test_decode_matches_oracle(G, R, page, fp8):
+    lens = [1, 0, 15, 16, 17, 63, 64, 65, 300, 1023]
+    c = make_cache(lens, G, page, fp8, seed=G * R)
+    q = torch.randn(len(lens), G * R, 128, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    out, lse = decode(c, q, lens)
+    check_decode(c, q, lens, out, lse)
+    assert (f64(out)[1] == 0).all() and np.isneginf(f64(lse)[1]).all()
+
+
+@pytest.mark.parametrize("lens,G,R", [([40000], 1, 4), ([20000, 3, 9000], 2, 8), ([1], 1, 1),
+                                      ([7] * 300, 1, 2), ([5000] * 5, 4, 16), ([2049] * 40, 8, 4)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_long_and_many(lens, G, R, fp8):
+    c = make_cache(lens, G, 32, fp8, seed=3)
+    q = torch.randn(len(lens), G * R, 128, generator=torch.Generator().manual_seed(2)).to(BF16).to(DEV)
+    ws = M.new_paged_workspace(M.MSA_OP_PAGED_DECODE, c["table"], 32, G * R, G)
+    out, lse = decode(c, q, lens, ws=ws)
+    check_decode(c, q, lens, out, lse)
+    again, lse2 = decode(c, q, lens, ws=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert M.msa_read_status(ws) == M.MSA_OK
+
+
+def test_decode_large_scores_and_scale():
+    """Scores of +-1000s: the running maximum carries them."""
+    lens = [700, 64]
+    c = make_cache(lens, 2, 64, False, seed=5, junk=True)
+    q = (100 * torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(2))).to(BF16).to(DEV)
+    out, lse = decode(c, q, lens, scale=0.3)
+    assert torch.isfinite(out).all()
+    ref = np.zeros(q.shape)
+    for b, n in enumerate(lens):
+        ref[b] = O.dense(f64(q[b])[None], gathered(c, "k", b, n), gathered(c, "v", b, n), [0, 1], [0, n], 0.3)[0][0]
+    # weights near 0 and 1: the score error itself is large here
+    assert np.abs(f64(out) - ref).max() < 0.1
+
+
+def test_decode_ascending_scores_move_the_maximum():
+    """Every tile raises the maximum: rescaling happens all the way."""
+    n = 3000
+    c = make_cache([n], 1, 64, False, seed=6)
+    k = torch.zeros_like(c["k"]).float()
+    t = torch.arange(n, device=DEV)
+    k[c["table"][0, t // 64].long(), t % 64, 0, 0] = torch.arange(n, device=DEV).float() / 100
+    c["k"] = k.to(BF16)
+    q = torch.zeros(1, 4, 128, device=DEV, dtype=BF16)
+    q[..., 0] = torch.tensor([16.0, -16.0, 1.0, 0.0], device=DEV)
+    out, lse = decode(c, q, [n])
+    check_decode(c, q, [n], out, lse)
+
+
+def test_decode_bad_lengths_and_pages():
+    lens = [100, 200, 150]
+    c = make_cache(lens, 2, 64, False, seed=7, junk=False)
+    c["table"][1, 1] = c["k"].shape[0]          # tokens 64..127 of sequence 1 have no page
+    q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(2)).to(BF16).to(DEV)
+    ws = M.new_paged_workspace(M.MSA_OP_PAGED_DECODE, c["table"], 64, 8, 2)
+    out, lse = decode(c, q, [100, 200, 100000], ws=ws)
+    assert M.msa_read_status(ws) == M.MSA_ERR_DEVICE_INPUT
+    assert M.msa_read_status(ws) == M.MSA_OK
+    assert (out[2] == 0).all() and torch.isneginf(lse[2]).all()
+    c["table"][1, 1] = 0
+    keep = [np.arange(100), np.r_[0:64, 128:200]]
+    check_decode(c, q[:2], lens[:2], out[:2], lse[:2], skip=keep)
+    out, lse = decode(c, q, [-1, 0, 150], ws=ws)
+    assert M.msa_read_status(ws) == M.MSA_ERR_DEVICE_INPUT
+    assert (out[:2] == 0).all() and torch.isfinite(lse[2]).all()
+
+
+# ------------------------------------------------------------------- append
+
+def check_append(lens, new, G, R, page, fp8, rot, inter, with_q=True, pad_rows=0, base=10000.0, inplace=False):
+    gen = torch.Generator().manual_seed(11)
+    one = new is None
+    cu = None if one else [0] + list(np.cumsum(new))
+    N = (len(lens) if one else cu[-1]) + pad_rows
+    c = make_cache(lens, G, page, fp8, seed=8, junk=False)
+    k, v = (torch.randn(N, G, 128, generator=gen).to(BF16).to(DEV) for _ in range(2))
+    v[0, 0] = 0                                  # an all-zero row: scale 1
+    q = torch.randn(N, G * R, 128, generator=gen).to(BF16).to(DEV) if with_q else None
+    f = (base ** (-torch.arange(max(1, rot // 2)).float() / max(1, rot // 2))).to(DEV)
+    before = {x: c[x].clone() for x in "kv"} | {x + "s": c[x + "s"].clone() if fp8 else None for x in "kv"}
+    k0, q0 = k.clone(), q.clone() if with_q else None
+    q_out = q if inplace else (torch.full_like(q, 3.0) if with_q else None)
+    k_out = k if inplace else torch.full_like(k, 3.0)
+    ws = M.new_paged_workspace(M.MSA_OP_PAGED_APPEND, c["table"], page, G * R, G)
+    r = M.msa_paged_append(k, v, c["k"], c["v"], c["table"], torch.tensor(lens, dtype=torch.int32, device=DEV),
+                           cu_new=None if one else torch.tensor(cu, dtype=torch.int32, device=DEV), q=q, q_out=q_out,
+                           k_out=k_out, inv_freq=f if rot else None, rot_dim=rot, interleaved=inter,
+                           k_scale=c["ks"], v_scale=c["vs"], ws=ws)
+    assert M.msa_read_status(ws) == M.MSA_OK
+    assert (r is None) == (not with_q)
+    rows = O.token_rows(lens, cu)
+    at, seq, pos = (np.array([x[i] for x in rows], dtype=int) for i in range(3))
+    table = c["table"].cpu().numpy()
+    pg, sl = table[seq, pos // page], pos % page
+    if rows:
+        assert np.array_equal(np.sort(pg * page + sl), np.unique(pg * page + sl))
+    for x, src in (("k", k0), ("v", v)):
+        want = f64(src)[at]
+        size = np.abs(want)
+        if x == "k":
+            want = O.rotate(want, pos, f64(f), rot, inter)
+            size = np.abs(want) + 0
+            if rot:
+                half = rot // 2
+                i0 = np.arange(half) * (2 if inter else 1)
+                i1 = i0 + (1 if inter else half)
+                ln = np.hypot(want[..., i0], want[..., i1])
+                size[..., i0], size[..., i1] = ln, ln
+            out = f64(k_out)
+            assert (np.abs(out[at] - want) <= O.U * np.abs(want) + 2.0 ** -20 * size).all()
+            rest = np.setdiff1d(np.arange(N), at)
+            assert np.array_equal(out[rest], (f64(k0) if inplace else np.full(out.shape, 3.0))[rest])
+        got = cache_f64(c, x)[pg, sl]
+        if fp8:
+            amax = np.abs(want).max(-1)
+            scale = np.where(amax > 0, amax / 448, 1.0)
+            assert (np.abs(f64(c[x + "s"])[pg, sl] - scale) <= 2.0 ** -19 * scale).all()
+            # half a step of a normal code is 2^-4 of it, of a subnormal one 2^-10 scales
+            tol = np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10 * scale[..., None]) * (1 + 2.0 ** -6)
+            tol += 2.0 ** -18 * size
+        else:
+            tol = O.U * np.abs(want) + 2.0 ** -20 * size
+        assert (np.abs(got - want) <= tol).all(), x
+        touched = torch.zeros(c[x].shape[:2], dtype=torch.bool)
+        touched[pg, sl] = True
+        same = (c[x].cpu().view(torch.uint8) == before[x].cpu().view(torch.uint8)).flatten(2).all(-1)
+        assert same[~touched].all(), "a row that no new token owns changed"
+        if fp8:
+            assert torch.equal(c[x + "s"].cpu()[~touched], before[x + "s"].cpu()[~touched])
+    if with_q:
+        want = O.rotate(f64(q0)[at], pos, f64(f), rot, inter)
+        got = f64(r)
+        assert (np.abs(got[at] - want) <= O.U * np.abs(want) + 2.0 ** -19 * np.abs(f64(q0)[at]).max()).all()
+        rest = np.setdiff1d(np.arange(N), at)
+        assert np.array_equal(got[rest], (f64(q0) if inplace else np.full(got.shape, 3.0))[rest])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rot,inter", [(128, False), (128, True), (64, False), (32, True), (16, False), (96, True),
+                                       (112, False), (0, False)])
+def test_append_rotations(rot, inter, fp8):
+    check_append([70, 300, 33], [70, 5, 1], 2, 4, 64, fp8, rot, inter)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G,R,page", [(1, 1, 16), (8, 4, 256), (3, 16, 32), (5, 2, 128)])
+def test_append_steps_and_heads(G, R, page, fp8):
+    check_append([1, 0, 16, 17, 512, 0, 1000], None, G, R, page, fp8, 128, False)
+
+
+def test_append_padding_and_no_queries():
+    check_append([20, 0, 9], [20, 4, 0], 2, 4, 16, False, 64, True, with_q=False, pad_rows=5)
+    check_append([20, 0, 9], [20, 4, 9], 2, 4, 16, True, 64, False, pad_rows=3)
+    check_append([40, 700], [40, 600], 2, 2, 64, False, 128, False, inplace=True)
+    check_append([40, 700], [40, 600], 2, 2, 64, True, 128, True, inplace=True)
+
+
+def test_append_many_rows():
+    check_append([3000, 1501, 900], [2990, 1501, 3], 4, 2, 64, False, 128, False)
+
+
+def test_append_far_positions():
+    """Angles at a million tokens: fp32 products would be off by 0.06 rad."""
+    n = 1 << 20
+    page, G = 256, 1
+    c = {x: torch.zeros(2, page, G, 128, dtype=BF16, device=DEV) for x in "kv"}
+    table = torch.full((1, n // page), -1, dtype=torch.int32)
+    table[0, -1] = 1
+    f = (1e6 ** (-torch.arange(64).float() / 64)).to(DEV)
+    k = torch.randn(3, G, 128, generator=torch.Generator().manual_seed(0)).to(BF16).to(DEV)
+    M.msa_paged_append(k, k, c["k"], c["v"], table.to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV),
+                       cu_new=torch.tensor([0, 3], dtype=torch.int32, device=DEV), inv_freq=f)
+    want = O.rotate(f64(k), np.arange(n - 3, n), f64(f), 128, False)
+    got = f64(c["k"])[1, page - 3:]
+    assert (np.abs(got - want) <= O.U * np.abs(want) + 2.0 ** -19 * np.abs(f64(k)).max()).all()
+
+
+def test_append_bad_input_is_skipped():
+    G, page = 1, 16
+    k = torch.ones(6, G, 128, dtype=BF16, device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+
+    def call(lens, cu, table):
+        pages = torch.zeros(4, page, G, 128, dtype=BF16, device=DEV)
+        t = torch.tensor(table, dtype=torch.int32, device=DEV)
+        M.msa_paged_append(k, k, pages, pages.clone(), t, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                           cu_new=torch.tensor(cu, dtype=torch.int32, device=DEV), ws=ws)
+        return M.msa_read_status(ws), (pages != 0).flatten(2).any(-1).nonzero().tolist()
+    good = [[0], [1]]
+    assert call([3, 3], [0, 3, 6], good) == (M.MSA_OK, [[0, 0], [0, 1], [0, 2], [1, 0], [1, 1], [1, 2]])
+    bad = M.MSA_ERR_DEVICE_INPUT
+    assert call([2, 3], [0, 3, 6], good) == (bad, [[1, 0], [1, 1], [1, 2]])    # fewer tokens than rows
+    assert call([17, 3], [0, 3, 6], good) == (bad, [[1, 0], [1, 1], [1, 2]])   # beyond the table
+    assert call([3, 3], [0, 3, 6], [[4], [1]]) == (bad, [[1, 0], [1, 1], [1, 2]])
+    assert call([3, 3], [0, 3, 6], [[-1], [1]]) == (bad, [[1, 0], [1, 1], [1, 2]])
+    assert call([3, 9], [0, 3, 9], good)[0] == bad                             # more rows than given
+    assert call([3, 3], [3, 0, 6], good)[0] == bad                             # descending
+    assert call([-3, 3], [0, 3, 6], good) == (bad, [[1, 0], [1, 1], [1, 2]])
