@@ -1,156 +1,583 @@
-// Dense causal attention over packed sequences: forward and backward.
+// Dense causal attention over packed sequences, forward.
 //   out = softmax(scale Q K^T) V per (sequence, head), the i-th of n query
 //   rows of a sequence with m keys seeing its first m - n + i + 1 keys.
 //
-//   dense_plan_kernel  checks cu_q and cu_k and writes each sequence's
-//                 {q0, nq, k0, nk}; a batch that is not ascending inside the
-//                 buffers is refused whole (every entry zero).
+//   dense_plan_kernel  checks cu_q and cu_k (a batch that is not ascending
+//                 inside the buffers is refused whole), writes each
+//                 sequence's {q0, nq, k0, nk} and the list of work items.
+//   dense_fwd_kernel   one work item is 256/R consecutive queries x the R
+//                 heads of one KV head: two 128-row tiles, A and B, that
+//                 sweep the same key tiles (128 keys) once:
+//                   S = Q K^T           UMMA into the tile's 128 TMEM columns
+//                   P = exp2(S - mr)    as bf16 over S's first 64 columns,
+//                                       mr a running reference maximum
+//                   O += P V            UMMA, A operand P from TMEM
+//
+// The tensor work of one (tile, key tile) is 2 x 128^3 products, 1024 cycles;
+// its 128 x 128 exponentials take 1024 cycles of the SM's 16-a-cycle unit.
+// So the two tiles take turns (one's softmax runs under the other's products)
+// and part of the exponentials go to the FMA pipe (f2_exp2_poly).
+//
+// Roles (one persistent CTA per SM, three warpgroups):
+//   warp 0     TMA producer: the tiles' Q, then K and V of each key tile, into
+//              a ring of five 32 KB tiles.
+//   warp 1     TMEM owner and MMA issuer.  Per key tile j: O_A += P_A V_j,
+//              S_A of j+1, O_B += P_B V_j, S_B of j+1.  UMMAs complete in
+//              issue order, so S_A may overwrite P_A behind the product that
+//              reads it, and a finished S_A(j+1) means a finished O_A(j).
+//   warps 4-7, 8-11  softmax of tile A and tile B, one row per thread.  mr
+//              moves only when a tile raises the row's maximum by more than
+//              2^8 in P; O and the row's sum are then scaled in place, a few
+//              times per row at most.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cfloat>
 
 #include "common.cuh"
+#include "dense.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace msa {
 
 namespace {
 
-__global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a) {
-  int bad = 0;
-  for (int b = threadIdx.x; b < a.B; b += 1024) {
+// ------------------------------------------------------------------ plan
+constexpr int kPlanBins = 1024;
+
+// Sum of v over the block's earlier threads, and the block's total.
+__device__ __forceinline__ int block_exclusive(int v, int *s_warp, int &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  __syncthreads();   // s_warp may still be read by the last call
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += x;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  total = s_warp[31];
+  return inc - v + (warp ? s_warp[warp - 1] : 0);
+}
+
+// One CTA.  Items are sorted by their number of key tiles, in at most 1024
+// steps of equal width (a counting sort; the order inside a step does not
+// matter, an item's result depends on nothing but the item).
+__global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int per) {
+  __shared__ int s_warp[32];
+  __shared__ int s_bin[kPlanBins];
+  const int tid = threadIdx.x;
+  grid_dep_launch();
+  int bad = 0, most = 0;
+  for (int b = tid; b < a.B; b += 1024) {
     const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
     bad |= q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk;
+    most = max(most, k1 - k0);
   }
   bad = __syncthreads_or(bad);
-  if (bad && threadIdx.x == 0) atomicCAS(a.status, 0, kStatusBadInput);
-  for (int b = threadIdx.x; b < a.B; b += 1024) {
-    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-    a.seqs[b] = bad ? make_int4(0, 0, 0, 0) : make_int4(q0, q1 - q0, k0, k1 - k0);
-  }
-}
-
-// The sequence that owns packed row r (by the starts in seqs[].x or, for
-// keys, seqs[].z): the last with start <= r.  False when r lies in none.
-template <bool KEY>
-__device__ __forceinline__ bool find_seq(const DenseArgs &a, int r, int4 &s) {
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((KEY ? a.seqs[mid].z : a.seqs[mid].x) <= r) lo = mid; else hi = mid - 1;
-  }
-  s = a.seqs[lo];
-  return KEY ? (r >= s.z && r < s.z + s.w) : (r >= s.x && r < s.x + s.y);
-}
-
-__device__ __forceinline__ float4 row4(const uint16_t *p, size_t row, int lane) {
-  const uint2 w = reinterpret_cast<const uint2 *>(p + row * kHeadDim)[lane];
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
-__device__ __forceinline__ float dot4(const float4 &x, const float4 &y) {
-  float z = x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  return z;
-}
-__device__ __forceinline__ void axpy4(float4 &y, float a, const float4 &x) {
-  y.x = fmaf(a, x.x, y.x);
-  y.y = fmaf(a, x.y, y.y);
-  y.z = fmaf(a, x.z, y.z);
-  y.w = fmaf(a, x.w, y.w);
-}
-__device__ __forceinline__ void put_row4(uint16_t *p, size_t row, int lane, const float4 &x, float f) {
-  reinterpret_cast<uint2 *>(p + row * kHeadDim)[lane] =
-      make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-}
-
-// One warp per (query row, head).
-__global__ void __launch_bounds__(256) dense_fwd_kernel(const DenseArgs a) {
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int r = int(w / a.H), h = int(w % a.H), g = h / (a.H / a.G);
-  int4 s;
-  if (r >= a.nq || !find_seq<false>(a, r, s)) return;
-  const int n_vis = s.w - s.y + (r - s.x) + 1;
-  const float4 q = row4(a.q, size_t(w), lane);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = 0; x < n_vis; ++x) {
-    const size_t kr = size_t(s.z + x) * a.G + g;
-    const float z = dot4(q, row4(a.k, kr, lane));
-    const float mn = fmaxf(m, z);
-    const float al = m == -INFINITY ? 0.f : exp2f((m - mn) * a.scale_log2);
-    const float p = exp2f((z - mn) * a.scale_log2);
-    m = mn;
-    l = l * al + p;
-    o.x *= al; o.y *= al; o.z *= al; o.w *= al;
-    axpy4(o, p, row4(a.v, kr, lane));
-  }
-  put_row4(a.out, size_t(w), lane, o, l > 0.f ? 1.f / l : 0.f);
-  if (a.lse && lane == 0) a.lse[w] = l > 0.f ? m * a.scale + logf(l) : -INFINITY;
-}
-
-// dq: one warp per (query row, head).
-__global__ void __launch_bounds__(256) dense_bwd_dq_kernel(const DenseArgs a) {
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int r = int(w / a.H), h = int(w % a.H), g = h / (a.H / a.G);
-  int4 s;
-  if (r >= a.nq || !find_seq<false>(a, r, s)) return;
-  const int n_vis = s.w - s.y + (r - s.x) + 1;
-  const float4 q = row4(a.q, size_t(w), lane), go = row4(a.dout, size_t(w), lane);
-  const float D = dot4(go, row4(a.out, size_t(w), lane));
-  const float lse2 = a.lse[w] * 1.4426950408889634f;
-  float4 dq = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = 0; x < n_vis; ++x) {
-    const size_t kr = size_t(s.z + x) * a.G + g;
-    const float4 k = row4(a.k, kr, lane);
-    const float p = exp2f(dot4(q, k) * a.scale_log2 - lse2);
-    axpy4(dq, p * (dot4(go, row4(a.v, kr, lane)) - D), k);
-  }
-  put_row4(a.dq, size_t(w), lane, dq, a.scale);
-}
-
-// dk, dv: one warp per (key row, KV head), over the query rows that see it.
-__global__ void __launch_bounds__(256) dense_bwd_dkv_kernel(const DenseArgs a) {
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int r = int(w / a.G), g = int(w % a.G), R = a.H / a.G;
-  int4 s;
-  if (r >= a.nk || !find_seq<true>(a, r, s)) return;
-  const float4 k = row4(a.k, size_t(w), lane), v = row4(a.v, size_t(w), lane);
-  float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
-  // query i sees key x = r - s.z when x <= nk - nq + i
-  for (int i = max(0, (r - s.z) - (s.w - s.y)); i < s.y; ++i)
-    for (int h = g * R; h < (g + 1) * R; ++h) {
-      const size_t qr = size_t(s.x + i) * a.H + h;
-      const float4 q = row4(a.q, qr, lane), go = row4(a.dout, qr, lane);
-      const float D = dot4(go, row4(a.out, qr, lane));
-      const float p = exp2f(dot4(q, k) * a.scale_log2 - a.lse[qr] * 1.4426950408889634f);
-      axpy4(dv, p, go);
-      axpy4(dk, p * (dot4(go, v) - D), q);
+  if (bad && tid == 0) atomicCAS(a.status, 0, kStatusBadInput);
+  s_bin[tid] = 0;
+  // the longest sequence sets the width of a step
+  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if ((tid & 31) == 0) s_warp[tid >> 5] = most;
+  __syncthreads();
+  for (int w = 0; w < 32; ++w) most = max(most, s_warp[w]);
+  const int width = ((most + 127) / 128) / kPlanBins + 1;
+  int base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+    const int b = b0 + tid;
+    int4 s = make_int4(0, 0, 0, 0);
+    if (b < a.B && !bad) {
+      s.x = a.cu_q[b];
+      s.y = a.cu_q[b + 1] - s.x;
+      s.z = a.cu_k[b];
+      s.w = a.cu_k[b + 1] - s.z;
     }
-  put_row4(a.dk, size_t(w), lane, dk, a.scale);
-  put_row4(a.dv, size_t(w), lane, dv, 1.f);
+    int total;
+    const int before = block_exclusive(ceil_div(s.y, per), s_warp, total);
+    if (b < a.B) {
+      a.seqs[b] = s;
+      a.prefix[b] = base + before;
+    }
+    base += total;
+  }
+  if (tid == 0) *a.n_items = base;
+  __syncthreads();
+  __threadfence_block();
+  // item x: its sequence (the last b with prefix[b] <= x) and place in it
+  auto item_of = [&](int x, int &bin) {
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.prefix[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    const int4 s = a.seqs[lo];
+    const int qt = x - a.prefix[lo];
+    const int seen = s.w - s.y + min(s.y, (qt + 1) * per);   // keys of the item's last row
+    bin = kPlanBins - 1 - min(kPlanBins - 1, max(0, (seen + 127) / 128) / width);
+    return make_int2(lo, qt);
+  };
+  for (int x = tid; x < base; x += 1024) {
+    int bin;
+    item_of(x, bin);
+    atomicAdd(&s_bin[bin], 1);
+  }
+  __syncthreads();
+  int total;
+  const int mine = s_bin[tid];
+  const int first = block_exclusive(mine, s_warp, total);
+  s_bin[tid] = first;
+  __syncthreads();
+  for (int x = tid; x < base; x += 1024) {
+    int bin;
+    const int2 it = item_of(x, bin);
+    const int at = atomicAdd(&s_bin[bin], 1);
+    if (at < a.max_items) a.items[at] = it;
+  }
 }
 
-unsigned warps_grid(long long warps) { return unsigned((warps + 7) / 8); }
+// ------------------------------------------------------------------ forward
+constexpr int kFThreads = 384;
+constexpr int kFTile = 32768;                    // 128 rows x 256 B
+constexpr int kFNkv = 5;                         // K/V ring depth
+constexpr int kFSQ = 0;                          // two Q tiles
+constexpr int kFSKV = 2 * kFTile;
+constexpr int kFCtl = kFSKV + kFNkv * kFTile;
+// barriers
+constexpr int kFQFull = 0, kFQEmpty = 2, kFKvFull = 4, kFKvEmpty = 4 + kFNkv,
+              kFSFull = 4 + 2 * kFNkv, kFPFull = kFSFull + 2, kFOFull = kFPFull + 2,
+              kFOEmpty = kFOFull + 2, kFDrain = kFOEmpty + 2, kFNumBars = kFDrain + 1;
+constexpr int kFCtlMisc = kFNumBars * 8;         // tmem holder, abort flag
+constexpr int kFSmem = kFCtl + kFCtlMisc + 16 + 1024;
+static_assert(kFSmem <= 232448, "shared memory budget");
+// TMEM columns: S (then P) of tile A and B, O of A and B
+constexpr uint32_t kFTmS = 0, kFTmO = 256;
+
+struct FItem {
+  int g, q0, k0, m;     // KV head, first packed query row, first key row, keys
+  int n;                // queries of both tiles
+  int hi0;              // last visible key of the first query
+  int n_kt_a, n_kt_b;   // key tiles of each tile
+  __device__ __forceinline__ int n_kt(int x) const { return x ? n_kt_b : n_kt_a; }
+};
+
+// Round r's item of this CTA (snake order over the CTAs), false at the end.
+// Items come longest first and every KV head of one before the next.
+template <int R>
+__device__ __forceinline__ bool dense_item(const DenseArgs &a, int r, int n_work, FItem &w) {
+  constexpr int QPI = 128 / R;
+  const int u = r * gridDim.x + ((r & 1) ? (gridDim.x - 1 - blockIdx.x) : blockIdx.x);
+  if (u >= n_work) return false;
+  const int2 it = a.items[u / a.G];
+  const int4 s = a.seqs[it.x];
+  w.g = u % a.G;
+  const int t0 = it.y * 2 * QPI;
+  w.q0 = s.x + t0;
+  w.k0 = s.z;
+  w.m = s.w;
+  w.n = min(2 * QPI, s.y - t0);
+  w.hi0 = s.w - s.y + t0;
+  const int last_a = w.hi0 + min(w.n, QPI) - 1, last_b = w.hi0 + w.n - 1;
+  w.n_kt_a = last_a >= 0 ? (last_a >> 7) + 1 : 0;
+  w.n_kt_b = (w.n > QPI && last_b >= 0) ? (last_b >> 7) + 1 : 0;
+  return true;
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One 16-byte store of eight fp32 values times f as bf16.
+__device__ __forceinline__ uint4 pack8_scaled(const float *x, float f) {
+  return make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
+                    pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f));
+}
+
+template <int R>
+__global__ void __launch_bounds__(kFThreads, 1)
+    dense_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const DenseArgs a) {
+  constexpr int QPI = 128 / R;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  const uint32_t s_base = smem_u32(smem);
+  uint8_t *ctl = smem + kFCtl;
+  const uint32_t bar0 = smem_u32(ctl);
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ctl + kFCtlMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(ctl + kFCtlMisc + 4);
+
+  const int tid = threadIdx.x;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int lane = tid & 31;
+  if (tid == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(kFQFull + x), 1);
+      mbar_init(bar(kFQEmpty + x), 1);
+      mbar_init(bar(kFSFull + x), 1);
+      mbar_init(bar(kFPFull + x), 128);
+      mbar_init(bar(kFOFull + x), 1);
+      mbar_init(bar(kFOEmpty + x), 128);
+    }
+    for (int x = 0; x < kFNkv; ++x) {
+      mbar_init(bar(kFKvFull + x), 1);
+      mbar_init(bar(kFKvEmpty + x), 1);
+    }
+    mbar_init(bar(kFDrain), 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  grid_dep_wait();   // the plan
+  const int n_work = *a.n_items * a.G;
+
+  if (warp < 4) {
+    regs_dec<72>();
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------- TMA producer
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      uint32_t kseq = 0, qn[2] = {0, 0};
+      bool ok = true;
+      FItem w;
+      for (int r = 0; ok && dense_item<R>(a, r, n_work, w); ++r) {
+        const int n_kt = max(w.n_kt_a, w.n_kt_b);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || w.n_kt(x) == 0) continue;
+          ok = mbar_wait(bar(kFQEmpty + x), (qn[x] & 1) ^ 1, abort_flag, a.status);
+          if (!ok) continue;
+          mbar_arrive_expect_tx(bar(kFQFull + x), kFTile);
+          const uint32_t dst = s_base + kFSQ + x * kFTile;
+          tma_load_3d(dst, &tm_q, bar(kFQFull + x), 0, w.g * R, w.q0 + x * QPI);
+          tma_load_3d(dst + 16384, &tm_q, bar(kFQFull + x), 64, w.g * R, w.q0 + x * QPI);
+          ++qn[x];
+        }
+        for (int step = 0; step < 2 * n_kt && ok; ++step) {
+          const int x = int(kseq % kFNkv);
+          ok = mbar_wait(bar(kFKvEmpty + x), ((kseq / kFNkv) & 1) ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(kFKvFull + x), kFTile);
+          const void *tm = (step & 1) ? static_cast<const void *>(&tm_v) : static_cast<const void *>(&tm_k);
+          const uint32_t dst = s_base + kFSKV + x * kFTile;
+          const int key0 = w.k0 + (step >> 1) * 128;
+          tma_load_3d(dst, tm, bar(kFKvFull + x), 0, w.g, key0);
+          tma_load_3d(dst + 16384, tm, bar(kFKvFull + x), 64, w.g, key0);
+          ++kseq;
+        }
+      }
+      // copies still in flight land before the CTA may exit
+      for (uint32_t x = 0; x < kFNkv; ++x)
+        if (kseq > x) {
+          const uint32_t last = kseq - 1 - x;
+          mbar_wait_drain(bar(kFKvFull + last % kFNkv), (last / kFNkv) & 1);
+        }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (qn[x]) mbar_wait_drain(bar(kFQFull + x), (qn[x] - 1) & 1);
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      // (the whole warp walks along: it clears the rows of V behind a
+      // sequence's last key, and lane 0 issues)
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);
+      uint32_t kseq = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
+      bool ok = true, issued = false;
+      FItem w;
+      auto kv_wait = [&](uint32_t seq) {
+        return mbar_wait(bar(kFKvFull + seq % kFNkv), (seq / kFNkv) & 1, abort_flag, a.status);
+      };
+      // S of tile x and key tile j (the ring's entry seq)
+      auto issue_s = [&](int x, int j, uint32_t seq) {
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t sq = s_base + kFSQ + x * kFTile;
+          const uint32_t sk = s_base + kFSKV + (seq % kFNkv) * kFTile;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+            umma_f16_ss(tmem_base + kFTmS + x * 128, sdesc_sw128(sq + off, 16, 1024),
+                        sdesc_sw128(sk + off, 16, 1024), idesc_s, kk > 0);
+          }
+          umma_commit(bar(kFSFull + x));
+          if (j + 1 == w.n_kt(x)) umma_commit(bar(kFQEmpty + x));
+          if (x == (j < w.n_kt_b ? 1 : 0)) umma_commit(bar(kFKvEmpty + seq % kFNkv));
+        }
+        issued = true;
+        __syncwarp();
+      };
+      for (int r = 0; ok && dense_item<R>(a, r, n_work, w); ++r) {
+        const int n_kt = max(w.n_kt_a, w.n_kt_b);
+        if (n_kt == 0) continue;
+        ok = kv_wait(kseq);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || w.n_kt(x) == 0) continue;
+          ok = mbar_wait(bar(kFQFull + x), qn[x] & 1, abort_flag, a.status);
+          if (!ok) continue;
+          ++qn[x];
+          issue_s(x, 0, kseq);
+        }
+        for (int j = 0; j < n_kt && ok; ++j) {
+          const uint32_t vseq = kseq + 2 * j + 1;
+          ok = kv_wait(vseq);
+          if (!ok) break;
+          const int rem = w.m - j * 128;       // keys of the sequence from this tile on
+          if (rem < 128) {
+            // rows behind the last key belong to others: their weights are
+            // 0, but 0 times a NaN there would not be
+            uint8_t *sv = smem + kFSKV + (vseq % kFNkv) * kFTile;
+            for (int i = rem * 8 + lane; i < 1024; i += 32) {
+              *reinterpret_cast<uint4 *>(sv + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4 *>(sv + 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= w.n_kt(x)) continue;
+            ok = mbar_wait(bar(kFPFull + x), pn[x] & 1, abort_flag, a.status);
+            if (ok && j == 0) ok = mbar_wait(bar(kFOEmpty + x), (on[x] & 1) ^ 1, abort_flag, a.status);
+            if (!ok) continue;
+            ++pn[x];
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t sv = s_base + kFSKV + (vseq % kFNkv) * kFTile;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)   // 16 keys per step, 8 columns of P
+                umma_f16_ts(tmem_base + kFTmO + x * 128, tmem_base + kFTmS + x * 128 + kk * 8,
+                            sdesc_sw128(sv + kk * 2048, 16384, 1024), idesc_o, (j > 0 || kk > 0));
+              if (x == (j < w.n_kt_b ? 1 : 0)) umma_commit(bar(kFKvEmpty + vseq % kFNkv));
+              if (j + 1 == w.n_kt(x)) umma_commit(bar(kFOFull + x));
+            }
+            issued = true;
+            __syncwarp();
+            if (j + 1 < w.n_kt(x)) {
+              ok = kv_wait(vseq + 1);
+              if (ok) issue_s(x, j + 1, vseq + 1);
+            } else {
+              ++on[x];
+            }
+          }
+        }
+        kseq += 2 * n_kt;
+      }
+      // every UMMA issued has completed before TMEM can be released
+      if (issued && lane == 0) {
+        umma_commit(bar(kFDrain));
+        mbar_wait_drain(bar(kFDrain), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    regs_inc<216>();
+    const int x = (warp - 4) >> 2;              // tile A or B
+    const int row = (warp & 3) * 32 + lane;     // tile row = TMEM lane
+    const uint32_t tm_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t tm_s = tm_lane + kFTmS + x * 128, tm_o = tm_lane + kFTmO + x * 128;
+    const int qi = row / R, hh = row % R;
+    const float2 sc2 = f2_dup(a.scale_log2);
+    uint32_t sn = 0, on = 0;
+    bool ok = true;
+    FItem w;
+    for (int r = 0; ok && dense_item<R>(a, r, n_work, w); ++r) {
+      const bool valid = x * QPI + qi < w.n;
+      const int n_kt = w.n_kt(x);
+      const int hi = valid ? w.hi0 + x * QPI + qi : -1;     // last visible key
+      const size_t orow = size_t(w.q0 + x * QPI + qi) * a.H + w.g * R + hh;
+      if (n_kt == 0) {                               // no row of the tile sees a key
+        if (valid) {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (a.lse) a.lse[orow] = -INFINITY;
+        }
+        continue;
+      }
+      float mr = -INFINITY;                          // reference maximum, raw scores
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int j = 0; j < n_kt; ++j) {
+        ok = mbar_wait(bar(kFSFull + x), sn & 1, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        ++sn;
+        tc_fence_after();
+        float v[128];
+        {
+          float t0[32], t1[32], t2[32], t3[32];
+          tmem_ld32(tm_s, t0);
+          tmem_ld32(tm_s + 32, t1);
+          tmem_ld32(tm_s + 64, t2);
+          tmem_ld32(tm_s + 96, t3);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            v[c] = t0[c];
+            v[32 + c] = t1[c];
+            v[64 + c] = t2[c];
+            v[96 + c] = t3[c];
+          }
+        }
+        const int lim = hi - j * 128;                // last visible column
+        const bool masked = __any_sync(0xffffffffu, lim < 127);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) v[c] = (c <= lim) ? v[c] : -INFINITY;
+        }
+        float mc[4];
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) mc[c4] = max3(v[32 * c4], v[32 * c4 + 1], v[32 * c4 + 2]);
+#pragma unroll
+        for (int c = 3; c + 2 <= 31; c += 2)
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) mc[c4] = max3(mc[c4], v[32 * c4 + c], v[32 * c4 + c + 1]);
+        float tmx = fmaxf(max3(mc[0], mc[1], v[31]), max3(mc[2], mc[3], v[63]));
+        tmx = max3(tmx, v[95], v[127]);
+        const bool resc = tmx > -INFINITY && (mr == -INFINITY || (tmx - mr) * a.scale_log2 > 8.f);
+        if (__any_sync(0xffffffffu, resc)) {
+          const float alpha = resc ? (mr == -INFINITY ? 0.f : fast_exp2((mr - tmx) * a.scale_log2)) : 1.f;
+          if (resc) mr = tmx;
+          l2 = f2_mul(l2, f2_dup(alpha));
+          if (j > 0) {
+            // S of this tile is complete, so the products into O before it are
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              float t0[32];
+              tmem_ld32(tm_o + c, t0);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) t0[e] *= alpha;
+              tmem_st32(tm_o + c, t0);
+            }
+          }
+        }
+        const float2 nmb2 = f2_dup(mr == -INFINITY ? 0.f : -mr * a.scale_log2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int c = h * 64 + 2 * e;
+            const float2 z = f2_fma(make_float2(v[c], v[c + 1]), sc2, nmb2);
+            const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+            l2 = f2_add(l2, p);
+            pw[e] = pack_bf16x2(p.x, p.y);
+          }
+          tmem_st32u(tm_s + h * 32, pw);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kFPFull + x));
+      }
+      if (!ok) break;
+      // ---- O / l
+      ok = mbar_wait(bar(kFOFull + x), on & 1, abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      ++on;
+      tc_fence_after();
+      float o[128];
+      {
+        float t0[32], t1[32], t2[32], t3[32];
+        tmem_ld32(tm_o, t0);
+        tmem_ld32(tm_o + 32, t1);
+        tmem_ld32(tm_o + 64, t2);
+        tmem_ld32(tm_o + 96, t3);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          o[c] = t0[c];
+          o[32 + c] = t1[c];
+          o[64 + c] = t2[c];
+          o[96 + c] = t3[c];
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(kFOEmpty + x));
+      if (valid) {
+        const float l = l2.x + l2.y;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) dst[c] = pack8_scaled(o + 8 * c, inv);
+        if (a.lse) a.lse[orow] = l > 0.f ? mr * a.scale + logf(l) : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int R>
+cudaError_t launch_fwd_r(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                         const DenseArgs &a, int num_sms, cudaStream_t st) {
+  auto kern = dense_fwd_kernel<R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFSmem);
+  if (e != cudaSuccess) return e;
+  const long long work = (long long)a.max_items * a.G;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(work < num_sms ? work : num_sms));
+  cfg.blockDim = dim3(kFThreads);
+  cfg.dynamicSmemBytes = kFSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a);
+}
 
 }  // namespace
 
-cudaError_t launch_dense_varlen(const DenseArgs &a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  dense_plan_kernel<<<1, 1024, 0, st>>>(a);
-  dense_fwd_kernel<<<warps_grid((long long)a.nq * a.H), 256, 0, st>>>(a);
+cudaError_t launch_dense_plan(const DenseArgs &a, cudaStream_t st) {
+  dense_plan_kernel<<<1, 1024, 0, st>>>(a, dense_item_queries(a.H / a.G));
   return cudaGetLastError();
 }
 
-cudaError_t launch_dense_varlen_backward(const DenseArgs &a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  dense_plan_kernel<<<1, 1024, 0, st>>>(a);
-  if (a.nq > 0) dense_bwd_dq_kernel<<<warps_grid((long long)a.nq * a.H), 256, 0, st>>>(a);
-  if (a.nk > 0) dense_bwd_dkv_kernel<<<warps_grid((long long)a.nk * a.G), 256, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_dense_varlen(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                const DenseArgs &a, int num_sms, cudaStream_t st) {
+  cudaError_t e = launch_dense_plan(a, st);
+  if (e != cudaSuccess) return e;
+  switch (a.H / a.G) {
+    case 1: return launch_fwd_r<1>(tq, tk, tv, a, num_sms, st);
+    case 2: return launch_fwd_r<2>(tq, tk, tv, a, num_sms, st);
+    case 4: return launch_fwd_r<4>(tq, tk, tv, a, num_sms, st);
+    case 8: return launch_fwd_r<8>(tq, tk, tv, a, num_sms, st);
+    case 16: return launch_fwd_r<16>(tq, tk, tv, a, num_sms, st);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace msa

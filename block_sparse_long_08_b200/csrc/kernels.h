@@ -243,20 +243,27 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int num_sms, cudaStrea
 
 // Dense attention over packed sequences (dense_kernels.cu).  The plan kernel
 // checks cu_q and cu_k and writes each sequence's {q0, nq, k0, nk} (all zero
-// when the batch is refused).
+// when the batch is refused) and the list of work items, longest first.
 struct DenseArgs {
   int B, H, G, nq, nk;
   float scale, scale_log2;
   const uint16_t *q, *k, *v;   // packed rows [nq,H,d], [nk,G,d]
   const int32_t *cu_q, *cu_k;  // [B+1]
   int4 *seqs;                  // [B]
+  int *prefix;                 // [B+1]: items of the sequences before b
+  int2 *items;                 // {sequence, query item}, longest first
+  int *n_items;
+  int max_items;               // entries of `items`
   uint16_t *out;               // [nq,H,d] (read by the backward)
   float *lse;                  // [nq,H] or null
   const uint16_t *dout;        // backward
   uint16_t *dq, *dk, *dv;
   int *status;
 };
-cudaError_t launch_dense_varlen(const DenseArgs &a, int num_sms, cudaStream_t st);
+// Queries of one forward work item: two 128-row tiles of 128/R queries x R heads.
+inline int dense_item_queries(int R) { return 256 / R; }
+cudaError_t launch_dense_varlen(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                const DenseArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_dense_varlen_backward(const DenseArgs &a, int num_sms, cudaStream_t st);
 
 // Sets the message msa_last_error() returns; returns `code`.

@@ -652,14 +652,22 @@ bool dense_op(int op) { return op >= MSA_OP_PAGED_APPEND && op <= MSA_OP_DENSE_V
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Packed-sequence operations: {q0, nq, k0, nk} per sequence.
+// Packed-sequence operations: {q0, nq, k0, nk} per sequence, the count and
+// the prefix of its work items, and their list (as many as p->L packed query
+// rows and one more per sequence can make).
 struct DenseWs {
-  size_t seqs, end;
+  size_t seqs, count, prefix, items, end;
+  int max_items;
 };
 DenseWs dense_ws(const msa_params *p) {
   DenseWs w;
+  const int per = msa::dense_item_queries(p->H / p->G);
+  w.max_items = p->L / per + p->B;
   size_t o = msa::kWsHeader;
   w.seqs = o; o = align_up(o + sizeof(int4) * size_t(p->B));
+  w.count = o; o = align_up(o + 4);
+  w.prefix = o; o = align_up(o + 4 * (size_t(p->B) + 1));
+  w.items = o; o = align_up(o + sizeof(int2) * size_t(w.max_items));
   w.end = o;
   return w;
 }
@@ -694,6 +702,27 @@ int check_cache(const msa_params *p, const msa_paged_cache *c, msa::PagedCache *
   return MSA_OK;
 }
 
+// 3-D map over packed query rows [nq,H,d] as (d, H, nq): a box is 128/R
+// consecutive queries x the R heads of one group, half of d.
+int make_packed_q_tmap(CUtensorMap *m, const void *q, const msa_params *p, int nq) {
+  const int r = p->H / p->G;
+  const uint64_t dims[3] = {uint64_t(p->d), uint64_t(p->H), uint64_t(nq)};
+  const uint64_t str[2] = {uint64_t(p->d) * 2, uint64_t(p->d) * 2 * p->H};
+  const uint32_t box[3] = {64, uint32_t(r), uint32_t(128 / r)};
+  return make_tmap(m, q, 3, dims, str, box);
+}
+
+// 3-D map over packed key rows [nk,G,d] as (d, G, nk): a box is 128 rows of
+// one KV head, half of d.  Without keys (nothing is loaded then) the map
+// stands over one row of `any`.
+int make_packed_kv_tmap(CUtensorMap *m, const void *base, const msa_params *p, int nk,
+                        const void *any) {
+  const uint64_t dims[3] = {uint64_t(p->d), uint64_t(p->G), uint64_t(nk > 0 ? nk : 1)};
+  const uint64_t str[2] = {uint64_t(p->d) * 2, uint64_t(p->d) * 2 * p->G};
+  const uint32_t box[3] = {64, 1, 128};
+  return make_tmap(m, nk > 0 ? base : any, 3, dims, str, box);
+}
+
 // Checks and arguments shared by the packed-sequence forward and backward.
 int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa_bf16 *k,
                const msa_bf16 *v, const int32_t *cu_q, const int32_t *cu_k, const void *out,
@@ -713,7 +742,12 @@ int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa
   a->scale_log2 = a->scale * 1.4426950408889634f;
   a->q = q; a->k = k; a->v = v;
   a->cu_q = cu_q; a->cu_k = cu_k;
-  a->seqs = reinterpret_cast<int4 *>(reinterpret_cast<uint8_t *>(ws) + w.seqs);
+  uint8_t *wsb = reinterpret_cast<uint8_t *>(ws);
+  a->seqs = reinterpret_cast<int4 *>(wsb + w.seqs);
+  a->n_items = reinterpret_cast<int *>(wsb + w.count);
+  a->prefix = reinterpret_cast<int *>(wsb + w.prefix);
+  a->items = reinterpret_cast<int2 *>(wsb + w.items);
+  a->max_items = nq / msa::dense_item_queries(p->H / p->G) + p->B;
   a->out = nullptr; a->lse = nullptr;
   a->dout = nullptr; a->dq = a->dk = a->dv = nullptr;
   a->status = status_ptr(ws);
@@ -1359,7 +1393,13 @@ int msa_dense_attn_varlen(const msa_params *p, int nq, int nk, const msa_bf16 *q
   if (nq == 0) return MSA_OK;
   a.out = out;
   a.lse = lse;
-  cudaError_t e = msa::launch_dense_varlen(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap tq, tk, tv;
+  rc = make_packed_q_tmap(&tq, q, p, nq);
+  if (!rc) rc = make_packed_kv_tmap(&tk, k, p, nk, q);
+  if (!rc) rc = make_packed_kv_tmap(&tv, v, p, nk, q);
+  if (rc) return rc;
+  cudaError_t e = msa::launch_dense_varlen(tq, tk, tv, a, num_sms(),
+                                           reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dense attention launch");
   return MSA_OK;
 }
