@@ -53,23 +53,4 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// 2^x of two values on the FMA pipe: x = n + f with n the nearest whole number
-// (adding 1.5 * 2^23 leaves n in the low mantissa bits), 2^f by a degree-4
-// polynomial whose largest relative error on [-1/2, 1/2] is 2.6e-6 (its
-// coefficients: a Remez exchange on that error), n added to the exponent.
-// For -126 <= x <= 126; smaller x is raised to -126.
-__device__ __forceinline__ float2 f2_exp2_poly(float2 x) {
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
-  const float2 magic = f2_dup(12582912.f);
-  const float2 t = f2_add(x, magic);
-  const float2 f = f2_add(x, f2_mul(f2_add(t, f2_dup(-12582912.f)), f2_dup(-1.f)));
-  float2 p = f2_fma(f2_dup(0.009570102207362652f), f, f2_dup(0.05591785907745361f));
-  p = f2_fma(p, f, f2_dup(0.240247443318367f));
-  p = f2_fma(p, f, f2_dup(0.6931217908859253f));
-  p = f2_fma(p, f, f2_dup(0.9999992847442627f));
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
-}
-
 }  // namespace msa

@@ -15,24 +15,34 @@
 //
 // The tensor work of one (tile, key tile) is 2 x 128^3 products, 1024 cycles;
 // its 128 x 128 exponentials take 1024 cycles of the SM's 16-a-cycle unit.
-// So the two tiles take turns (one's softmax runs under the other's products)
-// and part of the exponentials go to the FMA pipe (f2_exp2_poly).
+// The two tiles take turns: one's softmax runs under the other's products.
+// A tile's chain (softmax 1700 cycles, then O += P V and the next S, 1400
+// with the hand-overs) sets the pace: S and P share TMEM columns (2 x 128 for
+// S and 2 x 128 for O are all there is), so S cannot run ahead.  Measured:
+// 32K tokens, 8 heads on 1 KV head 1.94 ms (1136 TFLOP/s, 0.69 of burst
+// bf16).  Tried and slower: a quarter to half of the exponentials as
+// polynomials on the FMA pipe (1.98 ms at a quarter: an FMA pair takes two
+// issue slots), two softmax warpgroups per tile, an issuer per tile (the
+// products of both then finish late), S held back to interleave it with the
+// other tile's O (the tiles fall into step: 3.2 ms).
 //
 // Roles (one persistent CTA per SM, three warpgroups):
 //   warp 0     TMA producer: the tiles' Q, then K and V of each key tile, into
 //              a ring of five 32 KB tiles.
-//   warp 1     TMEM owner and MMA issuer.  Per key tile j: O_A += P_A V_j,
-//              S_A of j+1, O_B += P_B V_j, S_B of j+1.  UMMAs complete in
-//              issue order, so S_A may overwrite P_A behind the product that
-//              reads it, and a finished S_A(j+1) means a finished O_A(j).
+//   warp 1     TMEM owner; one thread issues the UMMAs.  Per key tile j:
+//              O_A += P_A V_j, S_A of j+1, O_B += P_B V_j, S_B of j+1.  UMMAs
+//              complete in issue order, so S_A may overwrite P_A behind the
+//              product that reads it, and a finished S_A(j+1) means a
+//              finished O_A(j).  What this thread does between two UMMAs is
+//              on the critical path: descriptors are stepped, not encoded,
+//              and the ring position is kept, not divided out (-15% time).
+//   warp 2     clears the rows of V behind a sequence's last key.
 //   warps 4-7, 8-11  softmax of tile A and tile B, one row per thread.  mr
 //              moves only when a tile raises the row's maximum by more than
 //              2^8 in P; O and the row's sum are then scaled in place, a few
 //              times per row at most.
 #include <cuda.h>
 #include <cuda_runtime.h>
-
-#include <cfloat>
 
 #include "common.cuh"
 #include "dense.cuh"
@@ -158,7 +168,8 @@ constexpr int kFCtl = kFSKV + kFNkv * kFTile;
 // barriers
 constexpr int kFQFull = 0, kFQEmpty = 2, kFKvFull = 4, kFKvEmpty = 4 + kFNkv,
               kFSFull = 4 + 2 * kFNkv, kFPFull = kFSFull + 2, kFOFull = kFPFull + 2,
-              kFOEmpty = kFOFull + 2, kFDrain = kFOEmpty + 2, kFNumBars = kFDrain + 1;
+              kFOEmpty = kFOFull + 2, kFDrain = kFOEmpty + 2, kFVReq = kFDrain + 1, kFVClean = kFVReq + 1,
+              kFNumBars = kFVClean + 1;
 constexpr int kFCtlMisc = kFNumBars * 8;         // tmem holder, abort flag
 constexpr int kFSmem = kFCtl + kFCtlMisc + 16 + 1024;
 static_assert(kFSmem <= 232448, "shared memory budget");
@@ -242,6 +253,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
       mbar_init(bar(kFKvEmpty + x), 1);
     }
     mbar_init(bar(kFDrain), 1);
+    mbar_init(bar(kFVReq), 1);
+    mbar_init(bar(kFVClean), 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -301,100 +314,117 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if (qn[x]) mbar_wait_drain(bar(kFQFull + x), (qn[x] - 1) & 1);
-    } else if (warp == 1) {
+    } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------- MMA issuer
-      // (the whole warp walks along: it clears the rows of V behind a
-      // sequence's last key, and lane 0 issues)
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);
-      uint32_t kseq = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
+      // operand descriptors: Q and K K-major, V MN-major
+      constexpr uint32_t kDescHi = sdesc_hi(1024);
+      const uint32_t q_lo = sdesc_lo(s_base + kFSQ, 16), k_lo = sdesc_lo(s_base + kFSKV, 16),
+                     v_lo = sdesc_lo(s_base + kFSKV, 16384);
+      // ring position of the next entry to be consumed, and its phase
+      uint32_t e = 0, ph = 0;
+      uint32_t qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0, cn = 0;   // phases: items and key tiles of A, B
       bool ok = true, issued = false;
       FItem w;
-      auto kv_wait = [&](uint32_t seq) {
-        return mbar_wait(bar(kFKvFull + seq % kFNkv), (seq / kFNkv) & 1, abort_flag, a.status);
+      auto step = [&](uint32_t &ek) {            // takes the next ring entry, once it is full
+        ok = ok && mbar_wait(bar(kFKvFull) + 8u * e, ph, abort_flag, a.status);
+        ek = e;
+        if (++e == kFNkv) { e = 0; ph ^= 1; }
       };
-      // S of tile x and key tile j (the ring's entry seq)
-      auto issue_s = [&](int x, int j, uint32_t seq) {
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t sq = s_base + kFSQ + x * kFTile;
-          const uint32_t sk = s_base + kFSKV + (seq % kFNkv) * kFTile;
+      // S of tile x from ring entry ek
+      auto issue_s = [&](int x, uint32_t ek, bool last_j, bool last_user) {
+        const uint32_t dq = q_lo + x * (kFTile >> 4), dk = k_lo + ek * (kFTile >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_f16_ss(tmem_base + kFTmS + x * 128, sdesc_sw128(sq + off, 16, 1024),
-                        sdesc_sw128(sk + off, 16, 1024), idesc_s, kk > 0);
-          }
-          umma_commit(bar(kFSFull + x));
-          if (j + 1 == w.n_kt(x)) umma_commit(bar(kFQEmpty + x));
-          if (x == (j < w.n_kt_b ? 1 : 0)) umma_commit(bar(kFKvEmpty + seq % kFNkv));
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          umma_f16_ss_w(tmem_base + kFTmS + x * 128, dq + off, kDescHi, dk + off, kDescHi, idesc_s,
+                        kk > 0);
         }
+        umma_commit(bar(kFSFull + x));
+        if (last_user) umma_commit(bar(kFKvEmpty) + 8u * ek);
+        if (last_j) umma_commit(bar(kFQEmpty + x));
         issued = true;
-        __syncwarp();
       };
       for (int r = 0; ok && dense_item<R>(a, r, n_work, w); ++r) {
-        const int n_kt = max(w.n_kt_a, w.n_kt_b);
+        const int na = w.n_kt_a, nb = w.n_kt_b, n_kt = max(na, nb);
         if (n_kt == 0) continue;
-        ok = kv_wait(kseq);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || w.n_kt(x) == 0) continue;
-          ok = mbar_wait(bar(kFQFull + x), qn[x] & 1, abort_flag, a.status);
-          if (!ok) continue;
-          ++qn[x];
-          issue_s(x, 0, kseq);
+        uint32_t ek, ev;
+        step(ek);
+        if (na > 0) {
+          ok = ok && mbar_wait(bar(kFQFull), qn0, abort_flag, a.status);
+          if (ok) issue_s(0, ek, na == 1, nb == 0);
+        }
+        if (nb > 0) {
+          ok = ok && mbar_wait(bar(kFQFull + 1), qn1, abort_flag, a.status);
+          if (ok) issue_s(1, ek, nb == 1, true);
         }
         for (int j = 0; j < n_kt && ok; ++j) {
-          const uint32_t vseq = kseq + 2 * j + 1;
-          ok = kv_wait(vseq);
-          if (!ok) break;
-          const int rem = w.m - j * 128;       // keys of the sequence from this tile on
-          if (rem < 128) {
-            // rows behind the last key belong to others: their weights are
-            // 0, but 0 times a NaN there would not be
-            uint8_t *sv = smem + kFSKV + (vseq % kFNkv) * kFTile;
-            for (int i = rem * 8 + lane; i < 1024; i += 32) {
-              *reinterpret_cast<uint4 *>(sv + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4 *>(sv + 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+          step(ev);
+          if (j + 1 < n_kt) step(ek);
+          if (j + 1 == n_kt && w.m - j * 128 < 128) {   // V's rows behind the last key are cleared
+            mbar_arrive(bar(kFVReq));
+            ok = ok && mbar_wait(bar(kFVClean), cn, abort_flag, a.status);
+            cn ^= 1;
           }
+          const uint32_t dv = v_lo + ev * (kFTile >> 4);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (!ok || j >= w.n_kt(x)) continue;
-            ok = mbar_wait(bar(kFPFull + x), pn[x] & 1, abort_flag, a.status);
-            if (ok && j == 0) ok = mbar_wait(bar(kFOEmpty + x), (on[x] & 1) ^ 1, abort_flag, a.status);
-            if (!ok) continue;
-            ++pn[x];
+            const int mine = x ? nb : na;
+            uint32_t &pn = x ? pn1 : pn0, &qn = x ? qn1 : qn0;
+            if (j >= mine) continue;
+            if (j == 0) ok = ok && mbar_wait(bar(kFOEmpty + x), qn ^ 1, abort_flag, a.status);
+            ok = ok && mbar_wait(bar(kFPFull + x), pn, abort_flag, a.status);
+            if (!ok) break;
+            pn ^= 1;
             tc_fence_after();
-            if (lane == 0) {
-              const uint32_t sv = s_base + kFSKV + (vseq % kFNkv) * kFTile;
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)   // 16 keys per step, 8 columns of P
-                umma_f16_ts(tmem_base + kFTmO + x * 128, tmem_base + kFTmS + x * 128 + kk * 8,
-                            sdesc_sw128(sv + kk * 2048, 16384, 1024), idesc_o, (j > 0 || kk > 0));
-              if (x == (j < w.n_kt_b ? 1 : 0)) umma_commit(bar(kFKvEmpty + vseq % kFNkv));
-              if (j + 1 == w.n_kt(x)) umma_commit(bar(kFOFull + x));
-            }
-            issued = true;
-            __syncwarp();
-            if (j + 1 < w.n_kt(x)) {
-              ok = kv_wait(vseq + 1);
-              if (ok) issue_s(x, j + 1, vseq + 1);
+            for (int kk = 0; kk < 8; ++kk)   // 16 keys per step, 8 columns of P
+              umma_f16_ts_w(tmem_base + kFTmO + x * 128, tmem_base + kFTmS + x * 128 + kk * 8,
+                            dv + ((kk * 2048) >> 4), kDescHi, idesc_o, (j > 0 || kk > 0));
+            if (j + 1 < mine) {
+              issue_s(x, ek, j + 2 == mine, x == (j + 1 < nb ? 1 : 0));
             } else {
-              ++on[x];
+              umma_commit(bar(kFOFull + x));
+              qn ^= 1;
             }
+            if (x == (j < nb ? 1 : 0)) umma_commit(bar(kFKvEmpty) + 8u * ev);
           }
         }
-        kseq += 2 * n_kt;
       }
       // every UMMA issued has completed before TMEM can be released
-      if (issued && lane == 0) {
+      if (issued) {
         umma_commit(bar(kFDrain));
         mbar_wait_drain(bar(kFDrain), 0);
       }
-      __syncwarp();
+    } else if (warp == 2) {
+      // -------------------------------------------------------- V cleaner
+      // Rows of a V tile behind the sequence's last key belong to others:
+      // their weights are 0, but 0 times a NaN there would not be.  Only an
+      // item's last key tile can have such rows.  The MMA issuer asks once the
+      // tile has landed (so both look at the same use of its ring entry).
+      uint32_t kseq = 0, cn = 0;
+      bool ok = true;
+      FItem w;
+      for (int r = 0; ok && dense_item<R>(a, r, n_work, w); ++r) {
+        const int n_kt = max(w.n_kt_a, w.n_kt_b);
+        kseq += 2 * n_kt;
+        const int rem = w.m - (n_kt - 1) * 128;
+        if (n_kt == 0 || rem >= 128) continue;
+        const uint32_t seq = kseq - 1;
+        ok = mbar_wait(bar(kFVReq), cn, abort_flag, a.status) &&
+             mbar_wait(bar(kFKvFull + seq % kFNkv), (seq / kFNkv) & 1, abort_flag, a.status);
+        cn ^= 1;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        uint8_t *sv = smem + kFSKV + (seq % kFNkv) * kFTile;
+        for (int i = rem * 8 + lane; i < 1024; i += 32) {
+          *reinterpret_cast<uint4 *>(sv + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(sv + 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kFVClean));
+      }
     }
   } else {
     // ---------------------------------------------------------- softmax
@@ -423,7 +453,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         continue;
       }
       float mr = -INFINITY;                          // reference maximum, raw scores
-      float2 l2 = make_float2(0.f, 0.f);
+      float2 l2 = make_float2(0.f, 0.f), l3 = l2;
       for (int j = 0; j < n_kt; ++j) {
         ok = mbar_wait(bar(kFSFull + x), sn & 1, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -465,6 +495,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           const float alpha = resc ? (mr == -INFINITY ? 0.f : fast_exp2((mr - tmx) * a.scale_log2)) : 1.f;
           if (resc) mr = tmx;
           l2 = f2_mul(l2, f2_dup(alpha));
+          l3 = f2_mul(l3, f2_dup(alpha));
           if (j > 0) {
             // S of this tile is complete, so the products into O before it are
 #pragma unroll 1
@@ -479,6 +510,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
         }
         const float2 nmb2 = f2_dup(mr == -INFINITY ? 0.f : -mr * a.scale_log2);
+        // P as bf16 over S's first 64 columns (S is all in registers)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pw[32];
@@ -487,7 +519,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
             const int c = h * 64 + 2 * e;
             const float2 z = f2_fma(make_float2(v[c], v[c + 1]), sc2, nmb2);
             const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-            l2 = f2_add(l2, p);
+            if (e & 1) l3 = f2_add(l3, p); else l2 = f2_add(l2, p);
             pw[e] = pack_bf16x2(p.x, p.y);
           }
           tmem_st32u(tm_s + h * 32, pw);
@@ -521,7 +553,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       tc_fence_before();
       mbar_arrive(bar(kFOEmpty + x));
       if (valid) {
-        const float l = l2.x + l2.y;
+        const float l = (l2.x + l3.x) + (l2.y + l3.y);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim);
 #pragma unroll
