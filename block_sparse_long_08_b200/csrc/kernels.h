@@ -237,8 +237,12 @@ struct PagedDecodeArgs {
   const int32_t *seq_lens;     // [B]
   uint16_t *out;               // [B,H,d]
   float *lse;                  // [B,H] or null
+  float *parts;                // two parts per CTA of paged_decode_kernel
+  int4 *meta;                  // per CTA: the pair it leaves unfinished {b, g, last CTA, -} or b -1
   int *status;
 };
+size_t paged_decode_parts_floats(int R);
+int paged_decode_max_ctas();
 cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int num_sms, cudaStream_t st);
 
 // Dense attention over packed sequences (dense_kernels.cu).  The plan kernel

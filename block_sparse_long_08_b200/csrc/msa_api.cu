@@ -672,7 +672,21 @@ DenseWs dense_ws(const msa_params *p) {
   return w;
 }
 
+// Single-token attention: the parts of sequences that cross CTAs.
+struct PagedDecWs {
+  size_t meta, parts, end;
+};
+PagedDecWs paged_dec_ws(const msa_params *p) {
+  PagedDecWs w;
+  size_t o = msa::kWsHeader;
+  w.meta = o; o = align_up(o + sizeof(int4) * size_t(msa::paged_decode_max_ctas()));
+  w.parts = o; o = align_up(o + 4 * msa::paged_decode_parts_floats(p->H / p->G));
+  w.end = o;
+  return w;
+}
+
 size_t dense_ws_bytes(const msa_params *p, int op) {
+  if (op == MSA_OP_PAGED_DECODE) return paged_dec_ws(p).end;
   if (op == MSA_OP_DENSE_VARLEN || op == MSA_OP_DENSE_VARLEN_BACKWARD) return dense_ws(p).end;
   return msa::kWsHeader;
 }
@@ -1367,8 +1381,11 @@ int msa_paged_attn_decode(const msa_params *p, const msa_paged_cache *c, const m
   if (!aligned16(q) || !aligned16(out) || !aligned4(seq_lens) || !aligned4(lse))
     return fail(MSA_ERR_INVALID_ARG,
                 "tensor pointers must be 16-byte aligned (seq_lens, lse 4-byte)");
-  rc = check_ws(ws, ws_bytes, dense_ws_bytes(p, MSA_OP_PAGED_DECODE));
+  const PagedDecWs w = paged_dec_ws(p);
+  rc = check_ws(ws, ws_bytes, w.end);
   if (rc) return rc;
+  a.meta = reinterpret_cast<int4 *>(reinterpret_cast<uint8_t *>(ws) + w.meta);
+  a.parts = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ws) + w.parts);
   a.B = p->B; a.Lmax = p->L; a.H = p->H; a.G = p->G;
   a.scale = eff_scale(p);
   a.scale_log2 = a.scale * 1.4426950408889634f;

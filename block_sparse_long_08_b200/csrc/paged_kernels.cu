@@ -3,12 +3,12 @@
 //
 //   paged_append_kernel  rotates the keys and queries of new tokens by their
 //                 position and writes keys and values into their cache rows.
-//   paged_decode_kernel  out = softmax(scale q K^T) V of one query row per
-//                 (sequence, head) over the sequence's cached tokens.
+//   paged_decode_kernel, paged_join_kernel  out = softmax(scale q K^T) V of
+//                 one query row per (sequence, head) over the sequence's
+//                 cached tokens, split over the SMs and joined.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
-
-#include <cfloat>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -182,107 +182,565 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
 }
 
 // ------------------------------------------------------------------ decode
-// Four values (dims 4 lane .. 4 lane + 3) of cache row `crow`, in fp32.
-template <bool FP8>
-__device__ __forceinline__ float4 cache_row4(const void *base, const float *scale, size_t crow,
-                                             int lane) {
-  if (FP8) {
-    const uint32_t w = reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(base) +
-                                                          crow * kHeadDim)[lane];
-    const float s = scale[crow];
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half_raw h = __nv_cvt_fp8_to_halfraw(uint8_t(w >> (8 * i)), __NV_E4M3);
-      f[i] = __half2float(__half(h)) * s;
-    }
-    return make_float4(f[0], f[1], f[2], f[3]);
-  }
-  const uint2 w = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) +
-                                                  crow * kHeadDim)[lane];
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+// The bytes of the cache bound this: 2 len G d of them per sequence, about R
+// products of each, far under the ridge; so mma.sync (heads as the 16 rows)
+// suffices for the products and the design is about keeping HBM busy.
+//   Work    The cache's 64-key tiles of all (sequence, KV head) pairs, in that
+//           order, are cut into equal runs, one per CTA (two CTAs per SM): no
+//           CTA waits for a longer sequence, whatever the lengths.  A pair
+//           that lies inside one run is finished by its CTA; of a pair that
+//           crosses runs every CTA leaves a part (O, maximum, sum in fp32)
+//           and paged_join_kernel adds them up.
+//   Loads   Each of the four warps owns 16 keys of a tile and runs its own
+//           cp.async ring over them (no block barrier inside a run).  Pages
+//           hold a multiple of 16 tokens, so a warp's step lies in one page.
+//   Sums    Per warp a running maximum, moved when a step exceeds it by more
+//           than 2^8 in P, and a sum, both fp32; P is rounded to bf16 for the
+//           product with V.
+constexpr int kPdTile = 64;                 // keys per tile, 16 per warp
+constexpr int kPdThreads = 128;
+constexpr int kPdMaxGrid = 512;             // CTAs, and so parts, at most
+constexpr int kPdRow = kHeadDim + 2;        // floats per head of a part: O, maximum, sum
+
+template <int R, bool FP8>
+struct PdCfg {
+  // a stage: 16 K rows and 16 V rows (8-bit: and their scales)
+  static constexpr int KB = 16 * kHeadDim * (FP8 ? 1 : 2);
+  static constexpr int STAGE = 2 * KB + (FP8 ? 128 : 0);
+  static constexpr int NST = FP8 ? 5 : 3;
+  static constexpr int SCR = FP8 ? 4096 : 0;   // a step's V rows as bf16
+  static constexpr int WARP = NST * STAGE + SCR;
+  static constexpr int OFF_O = 4 * WARP;       // [R][128] fp32
+  static constexpr int OFF_ML = OFF_O + R * kHeadDim * 4;   // [4][16] maxima, [4][16] sums
+  static constexpr int OFF_VIS = OFF_ML + 2 * 4 * 16 * 4;   // [4][NST] visible keys
+  static constexpr int SMEM = OFF_VIS + 4 * NST * 4;
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+__device__ __forceinline__ void cpa16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cpa4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cpa_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cpa_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two E4M3 codes (low byte first) as two f16 values (exact).
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t two) {
+  uint32_t r;
+  const uint16_t in = static_cast<uint16_t>(two);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(in));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t w) {
+  const __half2 h = __floats2half2_rn(bf16_lo(w), bf16_hi(w));
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// One CTA per (sequence, KV head); its four warps take the tokens in turn,
-// each with its own running maximum and sum per head, joined at the end.
+// Tokens of a sequence that are attended: 0 when its length is not allowed.
+__device__ __forceinline__ int pd_len(const PagedDecodeArgs &a, int b) {
+  const int n = a.seq_lens[b];
+  return (n < 0 || n > a.Lmax) ? 0 : n;
+}
+
+// A place in the list of tiles: (sequence, KV head, tile).
+struct PdCur {
+  int b, g, t, len;
+  __device__ __forceinline__ int tiles() const { return (len + kPdTile - 1) / kPdTile; }
+  __device__ __forceinline__ void seek(const PagedDecodeArgs &a) {   // the next sequence with tokens
+    while (b < a.B && (len = pd_len(a, b)) == 0) ++b;
+  }
+  __device__ __forceinline__ void next(const PagedDecodeArgs &a) {
+    if (++t < tiles()) return;
+    t = 0;
+    if (++g < a.G) return;
+    g = 0;
+    ++b;
+    seek(a);
+  }
+};
+
+// One chunk of 128 sequences from b0: this thread's tile count, those before
+// it in the chunk, and the chunk's total.
+__device__ __forceinline__ void pd_scan(const PagedDecodeArgs &a, int b0, long long *s_w, long long &mine,
+                                        long long &before, long long &total) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = b0 + tid;
+  mine = b < a.B ? (long long)((pd_len(a, b) + kPdTile - 1) / kPdTile) * a.G : 0;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) s_w[warp] = inc;
+  __syncthreads();
+  long long base = 0;
+  total = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < warp) base += s_w[w];
+    total += s_w[w];
+  }
+  before = base + inc - mine;
+  __syncthreads();
+}
+
 template <int R, bool FP8>
-__global__ void __launch_bounds__(128) paged_decode_kernel(const PagedDecodeArgs a) {
-  __shared__ float s_m[4][R], s_l[4][R];
-  __shared__ float s_o[4][R][kHeadDim];
-  const int b = blockIdx.x, g = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int n = a.seq_lens[b];
-  if (n < 0 || n > a.Lmax) {
-    if (threadIdx.x == 0) atomicCAS(a.status, 0, kStatusBadInput);
-    n = 0;
+__global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const PagedDecodeArgs a) {
+  using C = PdCfg<R, FP8>;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  __shared__ long long s_w[4];
+  __shared__ int s_start[3];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g4 = lane >> 2, c = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- this CTA's run of tiles [u0, u1)
+  long long T = 0, mine, before, total;
+  for (int b0 = 0; b0 < a.B; b0 += 128) {
+    pd_scan(a, b0, s_w, mine, before, total);
+    T += total;
   }
-  float m[R], l[R];
-  float4 o[R], q[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint2 w = reinterpret_cast<const uint2 *>(a.q + (size_t(b) * a.H + g * R + r) * kHeadDim)[lane];
-    q[r] = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-    o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int s = warp; s < n; s += 4) {
-    const int pg = a.c.table[size_t(b) * a.c.max_pages + (s >> a.c.page_log2)];
-    if (pg < 0 || pg >= a.c.num_pages) {
-      if (lane == 0) atomicCAS(a.status, 0, kStatusBadInput);
-      continue;
+  const int n_cta = int(T < gridDim.x ? T : gridDim.x);   // CTAs that get a run
+  const int cta = blockIdx.x;
+  const long long u0 = cta < n_cta ? T * cta / n_cta : 0, u1 = cta < n_cta ? T * (cta + 1) / n_cta : 0;
+  if (cta < n_cta) {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 128) {
+      if (a.B > 128) pd_scan(a, b0, s_w, mine, before, total);   // (else the one scan stands)
+      if (u0 >= base + before && u0 < base + before + mine) {
+        const int nt = int(mine / a.G);
+        const long long off = u0 - base - before;
+        s_start[0] = b0 + tid;
+        s_start[1] = int(off / nt);
+        s_start[2] = int(off % nt);
+      }
+      base += total;
+      if (base > u0) break;
     }
-    const size_t crow =
-        ((size_t(pg) << a.c.page_log2) + (s & ((1 << a.c.page_log2) - 1))) * a.G + g;
-    const float4 k = cache_row4<FP8>(a.c.k, a.c.k_scale, crow, lane);
-    const float4 v = cache_row4<FP8>(a.c.v, a.c.v_scale, crow, lane);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float z = q[r].x * k.x + q[r].y * k.y + q[r].z * k.z + q[r].w * k.w;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-      const float mn = fmaxf(m[r], z);
-      const float al = m[r] == -INFINITY ? 0.f : exp2f((m[r] - mn) * a.scale_log2);
-      const float p = exp2f((z - mn) * a.scale_log2);
-      m[r] = mn;
-      l[r] = l[r] * al + p;
-      o[r].x = o[r].x * al + p * v.x;
-      o[r].y = o[r].y * al + p * v.y;
-      o[r].z = o[r].z * al + p * v.z;
-      o[r].w = o[r].w * al + p * v.w;
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (lane == 0) { s_m[warp][r] = m[r]; s_l[warp][r] = l[r]; }
-    *reinterpret_cast<float4 *>(&s_o[warp][r][4 * lane]) = o[r];
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < R * kHeadDim; x += 128) {
-    const int r = x / kHeadDim, d = x % kHeadDim;
-    float M = -INFINITY;
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][r]);
-    float L = 0.f, O = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float e = s_m[w][r] == -INFINITY ? 0.f : exp2f((s_m[w][r] - M) * a.scale_log2);
-      L += e * s_l[w][r];
-      O += e * s_o[w][r][d];
+
+  int4 meta = make_int4(-1, 0, 0, 0);   // the pair that this CTA's run leaves unfinished
+  if (cta < n_cta) {
+    const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(dsm)) + warp * C::WARP;
+    uint8_t *smp = dsm + warp * C::WARP;
+    float *s_o = reinterpret_cast<float *>(dsm + C::OFF_O);
+    float *s_m = reinterpret_cast<float *>(dsm + C::OFF_ML), *s_l = s_m + 64;
+    volatile int *s_vis = reinterpret_cast<volatile int *>(dsm + C::OFF_VIS) + warp * C::NST;
+    const int pmask = (1 << a.c.page_log2) - 1;
+    PdCur ld;
+    ld.b = s_start[0]; ld.g = s_start[1]; ld.t = s_start[2];
+    ld.len = pd_len(a, ld.b);
+    PdCur cu = ld;
+    long long u_ld = u0;
+    auto page_of = [&](const PdCur &x) {
+      const int key = x.t * kPdTile + warp * 16;
+      return key < x.len ? a.c.table[size_t(x.b) * a.c.max_pages + (key >> a.c.page_log2)] : 0;
+    };
+    int pg = page_of(ld);
+    // copies of this warp's 16 keys of the next tile into ring stage st
+    auto issue = [&](int st) {
+      if (u_ld < u1) {
+        const int key = ld.t * kPdTile + warp * 16;
+        int vis = min(16, max(0, ld.len - key));
+        if (vis > 0 && (pg < 0 || pg >= a.c.num_pages)) {
+          vis = 0;
+          if (lane == 0) atomicCAS(a.status, 0, kStatusBadInput);
+        }
+        // (nothing is read where vis is 0: the row index stays inside the pool)
+        const size_t row = vis > 0 ? ((size_t(pg) << a.c.page_log2) + (key & pmask)) * a.G + ld.g : 0;
+        const uint32_t dst = sm + st * C::STAGE;
+        if (FP8) {
+          const int r0 = lane >> 3, gr = lane & 7;
+          const uint8_t *kp = static_cast<const uint8_t *>(a.c.k) + row * kHeadDim + gr * 16;
+          const uint8_t *vp = static_cast<const uint8_t *>(a.c.v) + row * kHeadDim + gr * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 4 * i;
+            const uint32_t n = r < vis ? 16u : 0u;
+            const size_t off = r < vis ? size_t(r) * a.G * kHeadDim : 0;
+            const uint32_t d = r * 128 + ((gr ^ ((r & 1) << 2)) << 4);
+            cpa16(dst + d, kp + off, n);
+            cpa16(dst + C::KB + d, vp + off, n);
+          }
+          const int r = lane & 15;
+          const float *sp = (lane < 16 ? a.c.k_scale : a.c.v_scale) + row + (r < vis ? size_t(r) * a.G : 0);
+          cpa4(dst + 2 * C::KB + lane * 4, sp, r < vis ? 4u : 0u);
+        } else {
+          const int r0 = lane >> 4, gr = lane & 15;
+          const uint16_t *kp = static_cast<const uint16_t *>(a.c.k) + row * kHeadDim + gr * 8;
+          const uint16_t *vp = static_cast<const uint16_t *>(a.c.v) + row * kHeadDim + gr * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 2 * i;
+            const uint32_t n = r < vis ? 16u : 0u;
+            const size_t off = r < vis ? size_t(r) * a.G * kHeadDim : 0;
+            const uint32_t d = r * 256 + ((gr ^ (r & 7)) << 4);
+            cpa16(dst + d, kp + off, n);
+            cpa16(dst + C::KB + d, vp + off, n);
+          }
+        }
+        if (lane == 0) s_vis[st] = vis;
+        ++u_ld;
+        if (u_ld < u1) {
+          ld.next(a);
+          pg = page_of(ld);   // used at the next issue
+        }
+      }
+      cpa_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < C::NST - 1; ++st) issue(st);
+
+    // running state of the pair: rows g4 and g4 + 8 of the 16 head rows
+    float o[16][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+    for (int d = 0; d < 16; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    uint32_t qf[8][4];
+    bool fresh = true;                              // a new pair: its queries are to be loaded
+    bool head = cu.t > 0;                           // the pair began in an earlier run
+    long long pair_left = 0;
+    int st = 0;
+    for (long long u = u0; u < u1; ++u) {
+      if (fresh) {
+        fresh = false;
+        pair_left = cu.tiles() - cu.t;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = g4 + (e & 1) * 8;
+            // bf16: dims 16 kk + 2c, +1 (e < 2) and + 8; 8-bit: the order in
+            // which a lane's sixteen codes of a granule feed four k steps
+            const int d = FP8 ? 16 * (c + 4 * (kk >> 2)) + 4 * (kk & 3) + (e >> 1) * 2 : kk * 16 + 2 * c + (e >> 1) * 8;
+            uint32_t w = 0;
+            if (r < R) w = *reinterpret_cast<const uint32_t *>(a.q + (size_t(cu.b) * a.H + cu.g * R + r) * kHeadDim + d);
+            qf[kk][e] = FP8 ? f16x2_of_bf16x2(w) : w;
+          }
+      }
+      cpa_wait<C::NST - 2>();
+      __syncwarp();
+      const int vis = s_vis[st];
+      const uint32_t kb = sm + st * C::STAGE, vb = kb + C::KB;
+      if (vis > 0) {
+        float s[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+        float vs[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+        if (FP8) {
+          const uint8_t *ks = smp + st * C::STAGE;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = i * 8 + g4;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(ks + r * 128 + (((c + 4 * h) ^ ((r & 1) << 2)) << 4));
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma_f16(s[i], qf[4 * h + x], f16x2_of_e4m3x2(ww[x]), f16x2_of_e4m3x2(ww[x] >> 16));
+            }
+          }
+          const float *sc = reinterpret_cast<const float *>(ks + 2 * C::KB);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 k2 = *reinterpret_cast<const float2 *>(sc + i * 8 + 2 * c);
+            const float2 v2 = *reinterpret_cast<const float2 *>(sc + 16 + i * 8 + 2 * c);
+            s[i][0] *= k2.x; s[i][1] *= k2.y; s[i][2] *= k2.x; s[i][3] *= k2.y;
+            vs[i][0] = v2.x; vs[i][1] = v2.y;
+          }
+          // V's codes as bf16 rows in the scratch, swizzled like a bf16 stage
+          const uint8_t *vr = smp + st * C::STAGE + C::KB;
+          uint8_t *scr = smp + C::NST * C::STAGE;
+          __syncwarp();   // the last step's reads of the scratch
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 3) + 4 * i, gr = lane & 7;
+            const uint4 w = *reinterpret_cast<const uint4 *>(vr + r * 128 + ((gr ^ ((r & 1) << 2)) << 4));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t x[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              x[2 * y] = bf16x2_of_f16x2(f16x2_of_e4m3x2(ww[y]));
+              x[2 * y + 1] = bf16x2_of_f16x2(f16x2_of_e4m3x2(ww[y] >> 16));
+            }
+            *reinterpret_cast<uint4 *>(scr + r * 256 + (((2 * gr) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4 *>(scr + r * 256 + (((2 * gr + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+          }
+          __syncwarp();
+        } else {
+          // matrices: (keys 0-7, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, ...), ...
+          const int r = (lane & 7) + ((lane >> 4) << 3), h = (lane >> 3) & 1;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            uint32_t b[4];
+            ldsm4(b, kb + r * 256 + (((2 * kk + h) ^ (r & 7)) << 4));
+            mma_bf16(s[0], qf[kk], b[0], b[1]);
+            mma_bf16(s[1], qf[kk], b[2], b[3]);
+          }
+        }
+        if (vis < 16) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (i * 8 + 2 * c + (e & 1) >= vis) s[i][e] = -INFINITY;
+        }
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+        for (int i = 1; i < 4; i <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, i));
+          if (R > 8) x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, i));
+        }
+        if (R <= 8) x1 = m1;   // rows 8-15 hold no head: their zeros move nothing
+        // (a step with a visible key has a finite maximum, so m0 and m1 are finite behind it)
+        const bool up0 = m0 == -INFINITY || (x0 - m0) * a.scale_log2 > 8.f;
+        const bool up1 = R > 8 && (m1 == -INFINITY || (x1 - m1) * a.scale_log2 > 8.f);
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+          const float al0 = up0 ? (m0 == -INFINITY ? 0.f : exp2_fast((m0 - x0) * a.scale_log2)) : 1.f;
+          const float al1 = up1 ? (m1 == -INFINITY ? 0.f : exp2_fast((m1 - x1) * a.scale_log2)) : 1.f;
+          if (up0) m0 = x0;
+          if (up1) m1 = x1;
+          l0 *= al0;
+          l1 *= al1;
+#pragma unroll
+          for (int d = 0; d < 16; ++d) {
+            o[d][0] *= al0; o[d][1] *= al0;
+            if (R > 8) { o[d][2] *= al1; o[d][3] *= al1; }
+          }
+        }
+        const float n0 = -m0 * a.scale_log2, n1 = R > 8 ? -m1 * a.scale_log2 : 0.f;
+        uint32_t pa[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p0 = exp2_fast(fmaf(s[i][0], a.scale_log2, n0)), p1 = exp2_fast(fmaf(s[i][1], a.scale_log2, n0));
+          l0 += p0 + p1;
+          pa[2 * i] = pack_bf16x2(p0 * vs[i][0], p1 * vs[i][1]);
+          if (R > 8) {
+            const float p2 = exp2_fast(fmaf(s[i][2], a.scale_log2, n1)), p3 = exp2_fast(fmaf(s[i][3], a.scale_log2, n1));
+            l1 += p2 + p3;
+            pa[2 * i + 1] = pack_bf16x2(p2 * vs[i][0], p3 * vs[i][1]);
+          } else {
+            pa[2 * i + 1] = 0;
+          }
+        }
+        // matrices: (keys 0-7, dims d), (keys 8-15, dims d), (keys 0-7, dims d + 8), ...
+        const int r = lane & 15, h = lane >> 4;
+        const uint32_t vrow = (FP8 ? sm + C::NST * C::STAGE : vb) + r * 256;
+#pragma unroll
+        for (int d = 0; d < 16; d += 2) {
+          uint32_t b[4];
+          ldsm4_t(b, vrow + (((d + h) ^ (r & 7)) << 4));
+          mma_bf16(o[d], pa, b[0], b[1]);
+          mma_bf16(o[d + 1], pa, b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      issue(st == 0 ? C::NST - 1 : st - 1);   // into the stage that was read last time
+      st = st + 1 == C::NST ? 0 : st + 1;
+
+      // ---- the pair's end, or the run's: join the four warps
+      const bool done = --pair_left == 0;
+      if (done || u + 1 == u1) {
+#pragma unroll
+        for (int i = 1; i < 4; i <<= 1) {
+          l0 += __shfl_xor_sync(0xffffffffu, l0, i);
+          l1 += __shfl_xor_sync(0xffffffffu, l1, i);
+        }
+        if (c == 0) {
+          s_m[warp * 16 + g4] = m0; s_m[warp * 16 + g4 + 8] = m1;
+          s_l[warp * 16 + g4] = l0; s_l[warp * 16 + g4 + 8] = l1;
+        }
+        __syncthreads();
+        float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          M0 = fmaxf(M0, s_m[w * 16 + g4]);
+          M1 = fmaxf(M1, s_m[w * 16 + g4 + 8]);
+        }
+        const float f0 = m0 == -INFINITY ? 0.f : exp2_fast((m0 - M0) * a.scale_log2);
+        const float f1 = m1 == -INFINITY ? 0.f : exp2_fast((m1 - M1) * a.scale_log2);
+        // warp by warp, so that the sum's order is always the same
+        for (int w = 0; w < 4; ++w) {
+          if (w == warp) {
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+              if (g4 < R) {
+                float2 *x = reinterpret_cast<float2 *>(s_o + g4 * kHeadDim + d * 8 + 2 * c);
+                const float2 y = w ? *x : make_float2(0.f, 0.f);
+                *x = make_float2(y.x + o[d][0] * f0, y.y + o[d][1] * f0);
+              }
+              if (g4 + 8 < R) {
+                float2 *x = reinterpret_cast<float2 *>(s_o + (g4 + 8) * kHeadDim + d * 8 + 2 * c);
+                const float2 y = w ? *x : make_float2(0.f, 0.f);
+                *x = make_float2(y.x + o[d][2] * f1, y.y + o[d][3] * f1);
+              }
+            }
+          }
+          __syncthreads();
+        }
+        const bool whole = done && !head;
+        // an unfinished pair: slot 0 when it began in an earlier run, else 1
+        float *part = a.parts + size_t(2 * cta + (head ? 0 : 1)) * R * kPdRow;
+        for (int r = 0; r < R; ++r) {
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w * 16 + r]);
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            L += s_m[w * 16 + r] == -INFINITY ? 0.f : s_l[w * 16 + r] * exp2_fast((s_m[w * 16 + r] - M) * a.scale_log2);
+          const float x = s_o[r * kHeadDim + tid];
+          if (whole) {
+            const size_t orow = size_t(cu.b) * a.H + cu.g * R + r;
+            reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + tid] = __float2bfloat16(L > 0.f ? x / L : 0.f);
+            if (tid == 0 && a.lse) a.lse[orow] = L > 0.f ? M * a.scale + logf(L) : -INFINITY;
+          } else {
+            part[r * kPdRow + tid] = x;
+            if (tid == 0) { part[r * kPdRow + kHeadDim] = M; part[r * kPdRow + kHeadDim + 1] = L; }
+          }
+        }
+        if (!done && !head) {
+          // the pair ends with tile u + pair_left; the CTA whose run holds that
+          const long long e = u + 1 + pair_left;
+          meta = make_int4(cu.b, cu.g, int((e * n_cta + T - 1) / T - 1), 0);
+        }
+        __syncthreads();   // s_o, s_m and s_l are free again
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+        fresh = true;
+        head = false;
+      }
+      if (u + 1 < u1) cu.next(a);
     }
-    const size_t row = size_t(b) * a.H + g * R + r;
-    reinterpret_cast<__nv_bfloat16 *>(a.out)[row * kHeadDim + d] =
-        __float2bfloat16(L > 0.f ? O / L : 0.f);
-    if (d == 0 && a.lse) a.lse[row] = L > 0.f ? M * a.scale + logf(L) : -INFINITY;
+    cpa_wait<0>();
   }
+  if (tid == 0) a.meta[cta] = meta;
+  // sequences without tokens: out 0, lse -inf (and a word about bad lengths)
+  for (int b = cta * 4 + warp; b < a.B; b += gridDim.x * 4) {
+    const int n = a.seq_lens[b];
+    if (n > 0 && n <= a.Lmax) continue;
+    if (n != 0 && lane == 0) atomicCAS(a.status, 0, kStatusBadInput);
+    for (int x = lane; x < a.H * (kHeadDim / 8); x += 32)
+      reinterpret_cast<uint4 *>(a.out + size_t(b) * a.H * kHeadDim)[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse)
+      for (int x = lane; x < a.H; x += 32) a.lse[size_t(b) * a.H + x] = -INFINITY;
+  }
+}
+
+// Joins the parts of the pair that CTA blockIdx.x of the decode left
+// unfinished (its slot 1, then slot 0 of the following CTAs), for one head:
+// out = sum_p 2^(s (M_p - M)) O_p / sum_p 2^(s (M_p - M)) L_p.
+__global__ void __launch_bounds__(512) paged_join_kernel(const PagedDecodeArgs a, int R) {
+  __shared__ float s_x[4][kHeadDim], s_l[4], s_max[16];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int cta = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+  const int4 meta = a.meta[cta];
+  if (meta.x < 0) return;
+  const int n = meta.z - cta + 1;
+  auto part = [&](int p) { return a.parts + (size_t(p == 0 ? 2 * cta + 1 : 2 * (cta + p)) * R + r) * kPdRow; };
+  float M = -INFINITY;
+  for (int p = tid; p < n; p += 512) M = fmaxf(M, __ldcg(part(p) + kHeadDim));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if ((tid & 31) == 0) s_max[tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) M = fmaxf(M, s_max[w]);
+  const int grp = tid >> 7, d = tid & 127;
+  float x = 0.f, l = 0.f;
+#pragma unroll 4
+  for (int p = grp; p < n; p += 4) {
+    const float *q = part(p);
+    const float mp = __ldcg(q + kHeadDim), lp = __ldcg(q + kHeadDim + 1), op = __ldcg(q + d);
+    const float f = mp == -INFINITY ? 0.f : exp2_fast((mp - M) * a.scale_log2);
+    x = fmaf(f, op, x);
+    l = fmaf(f, lp, l);
+  }
+  s_x[grp][d] = x;
+  if (d == 0) s_l[grp] = l;
+  __syncthreads();
+  if (grp) return;
+  x = (s_x[0][d] + s_x[1][d]) + (s_x[2][d] + s_x[3][d]);
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const size_t orow = size_t(meta.x) * a.H + meta.y * R + r;
+  reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + d] = __float2bfloat16(l > 0.f ? x / l : 0.f);
+  if (d == 0 && a.lse) a.lse[orow] = l > 0.f ? M * a.scale + logf(l) : -INFINITY;
+}
+
+template <int R, bool FP8>
+cudaError_t launch_decode_rt(const PagedDecodeArgs &a, int num_sms, cudaStream_t st) {
+  constexpr int smem = PdCfg<R, FP8>::SMEM;
+  auto kern = paged_decode_kernel<R, FP8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than tiles there can be (Lmax tokens in each sequence)
+  const long long most = (long long)a.B * a.G * ((a.Lmax + kPdTile - 1) / kPdTile);
+  int grid = 2 * num_sms < kPdMaxGrid ? 2 * num_sms : kPdMaxGrid;
+  if (most < grid) grid = most > 0 ? int(most) : 1;
+  kern<<<grid, kPdThreads, smem, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, R);
+  cfg.blockDim = dim3(512);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel, a, R);
 }
 
 template <int R>
-cudaError_t launch_decode_r(const PagedDecodeArgs &a, cudaStream_t st) {
-  const dim3 grid(a.B, a.G);
-  if (a.c.k_scale)
-    paged_decode_kernel<R, true><<<grid, 128, 0, st>>>(a);
-  else
-    paged_decode_kernel<R, false><<<grid, 128, 0, st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_decode_r(const PagedDecodeArgs &a, int num_sms, cudaStream_t st) {
+  return a.c.k_scale ? launch_decode_rt<R, true>(a, num_sms, st) : launch_decode_rt<R, false>(a, num_sms, st);
 }
 
 }  // namespace
@@ -297,15 +755,17 @@ cudaError_t launch_paged_append(const AppendArgs &a, int num_sms, cudaStream_t s
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs &a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
   switch (a.H / a.G) {
-    case 1: return launch_decode_r<1>(a, st);
-    case 2: return launch_decode_r<2>(a, st);
-    case 4: return launch_decode_r<4>(a, st);
-    case 8: return launch_decode_r<8>(a, st);
-    case 16: return launch_decode_r<16>(a, st);
+    case 1: return launch_decode_r<1>(a, num_sms, st);
+    case 2: return launch_decode_r<2>(a, num_sms, st);
+    case 4: return launch_decode_r<4>(a, num_sms, st);
+    case 8: return launch_decode_r<8>(a, num_sms, st);
+    case 16: return launch_decode_r<16>(a, num_sms, st);
     default: return cudaErrorInvalidValue;
   }
 }
+
+size_t paged_decode_parts_floats(int R) { return size_t(2) * kPdMaxGrid * R * kPdRow; }
+int paged_decode_max_ctas() { return kPdMaxGrid; }
 
 }  // namespace msa

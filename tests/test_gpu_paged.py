@@ -60,10 +60,10 @@ def cache_f64(c, x):
 
 
 def gathered(c, x, b, n):
-    w = cache_f64(c, x)
-    page = w.shape[1]
-    t = np.arange(n)
-    return w[c["table"].cpu().numpy()[b, t // page], t % page]
+    page = c[x].shape[1]
+    t = torch.arange(n, device=DEV)
+    at = (c["table"][b, t // page].long(), t % page)
+    return cache_f64({x: c[x][at], x + "s": None if c[x + "s"] is None else c[x + "s"][at]}, x)
 
 
 def decode(c, q, lens, **kw):
