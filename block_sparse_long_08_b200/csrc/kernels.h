@@ -238,7 +238,7 @@ struct PagedDecodeArgs {
   uint16_t *out;               // [B,H,d]
   float *lse;                  // [B,H] or null
   float *parts;                // two parts per CTA of paged_decode_kernel
-  int4 *meta;                  // per CTA: the pair it leaves unfinished {b, g, last CTA, -} or b -1
+  int4 *meta;                  // per CTA: the pair it leaves unfinished {b, g, parts, -} or b -1
   int *status;
 };
 size_t paged_decode_parts_floats(int R);

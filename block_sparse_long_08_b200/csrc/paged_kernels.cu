@@ -185,21 +185,24 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
 // The bytes of the cache bound this: 2 len G d of them per sequence, about R
 // products of each, far under the ridge; so mma.sync (heads as the 16 rows)
 // suffices for the products and the design is about keeping HBM busy.
-//   Work    The cache's 64-key tiles of all (sequence, KV head) pairs, in that
-//           order, are cut into equal runs, one per CTA (two CTAs per SM): no
-//           CTA waits for a longer sequence, whatever the lengths.  A pair
-//           that lies inside one run is finished by its CTA; of a pair that
-//           crosses runs every CTA leaves a part (O, maximum, sum in fp32)
-//           and paged_join_kernel adds them up.
+//   Work    The 64-key tiles of all sequences, in order, are cut into equal
+//           runs: no CTA waits for a longer sequence, whatever the lengths.
+//           A run goes to a group of G CTAs, one per KV head: they walk the
+//           same tokens side by side, whose rows (and 8-bit scales, 4 bytes
+//           of a sector each) lie next to each other.  A sequence inside one
+//           run is finished by its CTAs; of one that crosses runs every CTA
+//           leaves a part (O, maximum, sum in fp32) and paged_join_kernel
+//           adds them up.
 //   Loads   Each of the four warps owns 16 keys of a tile and runs its own
 //           cp.async ring over them (no block barrier inside a run).  Pages
 //           hold a multiple of 16 tokens, so a warp's step lies in one page.
 //   Sums    Per warp a running maximum, moved when a step exceeds it by more
 //           than 2^8 in P, and a sum, both fp32; P is rounded to bf16 for the
-//           product with V.
+//           product with V (8-bit: P times the value's scale to f16, the
+//           codes' own type in the product).
 constexpr int kPdTile = 64;                 // keys per tile, 16 per warp
 constexpr int kPdThreads = 128;
-constexpr int kPdMaxGrid = 512;             // CTAs, and so parts, at most
+constexpr int kPdMaxGrid = 1024;            // CTAs, and so parts, at most
 constexpr int kPdRow = kHeadDim + 2;        // floats per head of a part: O, maximum, sum
 
 template <int R, bool FP8>
@@ -207,14 +210,15 @@ struct PdCfg {
   // a stage: 16 K rows and 16 V rows (8-bit: and their scales)
   static constexpr int KB = 16 * kHeadDim * (FP8 ? 1 : 2);
   static constexpr int STAGE = 2 * KB + (FP8 ? 128 : 0);
-  static constexpr int NST = FP8 ? 5 : 3;
+  static constexpr int NST = 3;
+  static constexpr int CTAS = FP8 ? 3 : 2;   // per SM (8 bits: 3 measured 413 us, 2 438 us on 96 x <= 16K tokens)
   static constexpr int SCR = FP8 ? 4096 : 0;   // a step's V rows as bf16
   static constexpr int WARP = NST * STAGE + SCR;
   static constexpr int OFF_O = 4 * WARP;       // [R][128] fp32
   static constexpr int OFF_ML = OFF_O + R * kHeadDim * 4;   // [4][16] maxima, [4][16] sums
   static constexpr int OFF_VIS = OFF_ML + 2 * 4 * 16 * 4;   // [4][NST] visible keys
   static constexpr int SMEM = OFF_VIS + 4 * NST * 4;
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 };
 
 __device__ __forceinline__ void cpa16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -263,14 +267,18 @@ __device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t w) {
   const __half2 h = __floats2half2_rn(bf16_lo(w), bf16_hi(w));
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t w) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-  return pack_bf16x2(f.x, f.y);
-}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Byte of 16-byte granule gr of row r in a stage: rows of 256 bytes (8-bit:
+// 128), granules permuted so that eight rows of one granule (8-bit: two rows
+// of four granules) fall into different banks.
+template <bool FP8>
+__device__ __forceinline__ uint32_t swz(int r, int gr) {
+  return FP8 ? r * 128 + ((gr ^ ((r & 1) << 2)) << 4) : r * 256 + ((gr ^ (r & 7)) << 4);
 }
 
 // Tokens of a sequence that are attended: 0 when its length is not allowed.
@@ -279,9 +287,9 @@ __device__ __forceinline__ int pd_len(const PagedDecodeArgs &a, int b) {
   return (n < 0 || n > a.Lmax) ? 0 : n;
 }
 
-// A place in the list of tiles: (sequence, KV head, tile).
+// A place in the list of tiles: (sequence, tile).
 struct PdCur {
-  int b, g, t, len;
+  int b, t, len;
   __device__ __forceinline__ int tiles() const { return (len + kPdTile - 1) / kPdTile; }
   __device__ __forceinline__ void seek(const PagedDecodeArgs &a) {   // the next sequence with tokens
     while (b < a.B && (len = pd_len(a, b)) == 0) ++b;
@@ -289,8 +297,6 @@ struct PdCur {
   __device__ __forceinline__ void next(const PagedDecodeArgs &a) {
     if (++t < tiles()) return;
     t = 0;
-    if (++g < a.G) return;
-    g = 0;
     ++b;
     seek(a);
   }
@@ -302,7 +308,7 @@ __device__ __forceinline__ void pd_scan(const PagedDecodeArgs &a, int b0, long l
                                         long long &before, long long &total) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = b0 + tid;
-  mine = b < a.B ? (long long)((pd_len(a, b) + kPdTile - 1) / kPdTile) * a.G : 0;
+  mine = b < a.B ? (pd_len(a, b) + kPdTile - 1) / kPdTile : 0;
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -322,11 +328,11 @@ __device__ __forceinline__ void pd_scan(const PagedDecodeArgs &a, int b0, long l
 }
 
 template <int R, bool FP8>
-__global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const PagedDecodeArgs a) {
+__global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decode_kernel(const PagedDecodeArgs a) {
   using C = PdCfg<R, FP8>;
   extern __shared__ __align__(128) uint8_t dsm[];
   __shared__ long long s_w[4];
-  __shared__ int s_start[3];
+  __shared__ int s_start[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g4 = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -337,19 +343,17 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
     pd_scan(a, b0, s_w, mine, before, total);
     T += total;
   }
-  const int n_cta = int(T < gridDim.x ? T : gridDim.x);   // CTAs that get a run
-  const int cta = blockIdx.x;
-  const long long u0 = cta < n_cta ? T * cta / n_cta : 0, u1 = cta < n_cta ? T * (cta + 1) / n_cta : 0;
-  if (cta < n_cta) {
+  const int groups = gridDim.x / a.G;
+  const int n_grp = int(T < groups ? T : groups);         // groups that get a run
+  const int cta = blockIdx.x, grp = cta / a.G, g = cta % a.G;
+  const long long u0 = grp < n_grp ? T * grp / n_grp : 0, u1 = grp < n_grp ? T * (grp + 1) / n_grp : 0;
+  if (grp < n_grp) {
     long long base = 0;
     for (int b0 = 0; b0 < a.B; b0 += 128) {
       if (a.B > 128) pd_scan(a, b0, s_w, mine, before, total);   // (else the one scan stands)
       if (u0 >= base + before && u0 < base + before + mine) {
-        const int nt = int(mine / a.G);
-        const long long off = u0 - base - before;
         s_start[0] = b0 + tid;
-        s_start[1] = int(off / nt);
-        s_start[2] = int(off % nt);
+        s_start[1] = int(u0 - base - before);
       }
       base += total;
       if (base > u0) break;
@@ -357,8 +361,8 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
   }
   __syncthreads();
 
-  int4 meta = make_int4(-1, 0, 0, 0);   // the pair that this CTA's run leaves unfinished
-  if (cta < n_cta) {
+  int4 meta = make_int4(-1, 0, 0, 0);   // {b, g, parts} of the pair that this CTA's run leaves unfinished
+  if (grp < n_grp) {
     const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(dsm)) + warp * C::WARP;
     uint8_t *smp = dsm + warp * C::WARP;
     float *s_o = reinterpret_cast<float *>(dsm + C::OFF_O);
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
     volatile int *s_vis = reinterpret_cast<volatile int *>(dsm + C::OFF_VIS) + warp * C::NST;
     const int pmask = (1 << a.c.page_log2) - 1;
     PdCur ld;
-    ld.b = s_start[0]; ld.g = s_start[1]; ld.t = s_start[2];
+    ld.b = s_start[0]; ld.t = s_start[1];
     ld.len = pd_len(a, ld.b);
     PdCur cu = ld;
     long long u_ld = u0;
@@ -385,37 +389,36 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
           if (lane == 0) atomicCAS(a.status, 0, kStatusBadInput);
         }
         // (nothing is read where vis is 0: the row index stays inside the pool)
-        const size_t row = vis > 0 ? ((size_t(pg) << a.c.page_log2) + (key & pmask)) * a.G + ld.g : 0;
+        const size_t row = vis > 0 ? ((size_t(pg) << a.c.page_log2) + (key & pmask)) * a.G + g : 0;
         const uint32_t dst = sm + st * C::STAGE;
-        if (FP8) {
-          const int r0 = lane >> 3, gr = lane & 7;
-          const uint8_t *kp = static_cast<const uint8_t *>(a.c.k) + row * kHeadDim + gr * 16;
-          const uint8_t *vp = static_cast<const uint8_t *>(a.c.v) + row * kHeadDim + gr * 16;
+        // rows behind the visible ones are filled with zeros, not read
+        constexpr int GR = FP8 ? 8 : 16, ROWS = 32 / GR, EB = FP8 ? 1 : 2;
+        const int r0 = lane / GR, gr = lane % GR;
+        const size_t off0 = (row + size_t(r0 < vis ? r0 : 0) * a.G) * (kHeadDim * EB) + gr * 16;
+        const uint8_t *kp = static_cast<const uint8_t *>(a.c.k) + off0;
+        const uint8_t *vp = static_cast<const uint8_t *>(a.c.v) + off0;
+        const uint32_t stepb = uint32_t(a.G) * (ROWS * kHeadDim * EB);
+        if (vis == 16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 4 * i;
-            const uint32_t n = r < vis ? 16u : 0u;
-            const size_t off = r < vis ? size_t(r) * a.G * kHeadDim : 0;
-            const uint32_t d = r * 128 + ((gr ^ ((r & 1) << 2)) << 4);
-            cpa16(dst + d, kp + off, n);
-            cpa16(dst + C::KB + d, vp + off, n);
+          for (int i = 0; i < 16 / ROWS; ++i) {
+            const uint32_t d = swz<FP8>(r0 + ROWS * i, gr);
+            cpa16(dst + d, kp + i * size_t(stepb), 16u);
+            cpa16(dst + C::KB + d, vp + i * size_t(stepb), 16u);
           }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 16 / ROWS; ++i) {
+            const int r = r0 + ROWS * i;
+            const uint32_t d = swz<FP8>(r, gr), n = r < vis ? 16u : 0u;
+            const size_t o = r < vis ? i * size_t(stepb) : 0;
+            cpa16(dst + d, kp + o, n);
+            cpa16(dst + C::KB + d, vp + o, n);
+          }
+        }
+        if (FP8) {
           const int r = lane & 15;
           const float *sp = (lane < 16 ? a.c.k_scale : a.c.v_scale) + row + (r < vis ? size_t(r) * a.G : 0);
           cpa4(dst + 2 * C::KB + lane * 4, sp, r < vis ? 4u : 0u);
-        } else {
-          const int r0 = lane >> 4, gr = lane & 15;
-          const uint16_t *kp = static_cast<const uint16_t *>(a.c.k) + row * kHeadDim + gr * 8;
-          const uint16_t *vp = static_cast<const uint16_t *>(a.c.v) + row * kHeadDim + gr * 8;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 2 * i;
-            const uint32_t n = r < vis ? 16u : 0u;
-            const size_t off = r < vis ? size_t(r) * a.G * kHeadDim : 0;
-            const uint32_t d = r * 256 + ((gr ^ (r & 7)) << 4);
-            cpa16(dst + d, kp + off, n);
-            cpa16(dst + C::KB + d, vp + off, n);
-          }
         }
         if (lane == 0) s_vis[st] = vis;
         ++u_ld;
@@ -430,7 +433,8 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
     for (int st = 0; st < C::NST - 1; ++st) issue(st);
 
     // running state of the pair: rows g4 and g4 + 8 of the 16 head rows
-    float o[16][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // (8-bit: O is kept against mw, the others against m)
+    float o[16][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, mw0 = -INFINITY, mw1 = -INFINITY;
 #pragma unroll
     for (int d = 0; d < 16; ++d)
 #pragma unroll
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
             // which a lane's sixteen codes of a granule feed four k steps
             const int d = FP8 ? 16 * (c + 4 * (kk >> 2)) + 4 * (kk & 3) + (e >> 1) * 2 : kk * 16 + 2 * c + (e >> 1) * 8;
             uint32_t w = 0;
-            if (r < R) w = *reinterpret_cast<const uint32_t *>(a.q + (size_t(cu.b) * a.H + cu.g * R + r) * kHeadDim + d);
+            if (r < R) w = *reinterpret_cast<const uint32_t *>(a.q + (size_t(cu.b) * a.H + g * R + r) * kHeadDim + d);
             qf[kk][e] = FP8 ? f16x2_of_bf16x2(w) : w;
           }
       }
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
             const int r = i * 8 + g4;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(ks + r * 128 + (((c + 4 * h) ^ ((r & 1) << 2)) << 4));
+              const uint4 w = *reinterpret_cast<const uint4 *>(ks + swz<true>(r, c + 4 * h));
               const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int x = 0; x < 4; ++x)
@@ -490,23 +494,20 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
             s[i][0] *= k2.x; s[i][1] *= k2.y; s[i][2] *= k2.x; s[i][3] *= k2.y;
             vs[i][0] = v2.x; vs[i][1] = v2.y;
           }
-          // V's codes as bf16 rows in the scratch, swizzled like a bf16 stage
+          // V's codes as f16 rows in the scratch: the two granules that a
+          // granule of codes makes lie 128 bytes apart (no bank conflicts)
           const uint8_t *vr = smp + st * C::STAGE + C::KB;
           uint8_t *scr = smp + C::NST * C::STAGE;
           __syncwarp();   // the last step's reads of the scratch
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = (lane >> 3) + 4 * i, gr = lane & 7;
-            const uint4 w = *reinterpret_cast<const uint4 *>(vr + r * 128 + ((gr ^ ((r & 1) << 2)) << 4));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            uint32_t x[8];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              x[2 * y] = bf16x2_of_f16x2(f16x2_of_e4m3x2(ww[y]));
-              x[2 * y + 1] = bf16x2_of_f16x2(f16x2_of_e4m3x2(ww[y] >> 16));
-            }
-            *reinterpret_cast<uint4 *>(scr + r * 256 + (((2 * gr) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4 *>(scr + r * 256 + (((2 * gr + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+            const uint4 w = *reinterpret_cast<const uint4 *>(vr + swz<true>(r, gr));
+            uint4 *d = reinterpret_cast<uint4 *>(scr + r * 256 + ((gr ^ (r & 7)) << 4));
+            d[0] = make_uint4(f16x2_of_e4m3x2(w.x), f16x2_of_e4m3x2(w.x >> 16), f16x2_of_e4m3x2(w.y),
+                              f16x2_of_e4m3x2(w.y >> 16));
+            d[8] = make_uint4(f16x2_of_e4m3x2(w.z), f16x2_of_e4m3x2(w.z >> 16), f16x2_of_e4m3x2(w.w),
+                              f16x2_of_e4m3x2(w.w >> 16));
           }
           __syncwarp();
         } else {
@@ -545,36 +546,82 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
           if (up1) m1 = x1;
           l0 *= al0;
           l1 *= al1;
+          if (!FP8) {
 #pragma unroll
-          for (int d = 0; d < 16; ++d) {
-            o[d][0] *= al0; o[d][1] *= al0;
-            if (R > 8) { o[d][2] *= al1; o[d][3] *= al1; }
+            for (int d = 0; d < 16; ++d) {
+              o[d][0] *= al0; o[d][1] *= al0;
+              if (R > 8) { o[d][2] *= al1; o[d][3] *= al1; }
+            }
           }
         }
         const float n0 = -m0 * a.scale_log2, n1 = R > 8 ? -m1 * a.scale_log2 : 0.f;
         uint32_t pa[4];
+        float lv[2][2], w0 = 0.f, w1 = 0.f;
+        if (FP8) {
+          // the weights that multiply V's codes are P |scale|, in f16, against
+          // a reference of their own (log2): any scale keeps its 11 bits
+          float y0 = -INFINITY, y1 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float p0 = exp2_fast(fmaf(s[i][0], a.scale_log2, n0)), p1 = exp2_fast(fmaf(s[i][1], a.scale_log2, n0));
-          l0 += p0 + p1;
-          pa[2 * i] = pack_bf16x2(p0 * vs[i][0], p1 * vs[i][1]);
-          if (R > 8) {
-            const float p2 = exp2_fast(fmaf(s[i][2], a.scale_log2, n1)), p3 = exp2_fast(fmaf(s[i][3], a.scale_log2, n1));
-            l1 += p2 + p3;
-            pa[2 * i + 1] = pack_bf16x2(p2 * vs[i][0], p3 * vs[i][1]);
-          } else {
-            pa[2 * i + 1] = 0;
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              lv[i][e] = __log2f(fabsf(vs[i][e]));
+              y0 = fmaxf(y0, fmaf(s[i][e], a.scale_log2, lv[i][e]));
+              if (R > 8) y1 = fmaxf(y1, fmaf(s[i][2 + e], a.scale_log2, lv[i][e]));
+            }
+#pragma unroll
+          for (int i = 1; i < 4; i <<= 1) {
+            y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, i));
+            if (R > 8) y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, i));
           }
+          const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > 8.f);
+          const bool wu1 = R > 8 && y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > 8.f);
+          if (__any_sync(0xffffffffu, wu0 || wu1)) {
+            const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - y0)) : 1.f;
+            const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - y1)) : 1.f;
+            if (wu0) mw0 = y0;
+            if (wu1) mw1 = y1;
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+              o[d][0] *= al0; o[d][1] *= al0;
+              if (R > 8) { o[d][2] *= al1; o[d][3] *= al1; }
+            }
+          }
+          w0 = mw0 == -INFINITY ? 0.f : -mw0;
+          w1 = mw1 == -INFINITY ? 0.f : -mw1;
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < (R > 8 ? 2 : 1); ++h) {   // rows g4, then g4 + 8
+            const float z0 = s[i][2 * h] * a.scale_log2, z1 = s[i][2 * h + 1] * a.scale_log2;
+            const float n = h ? n1 : n0, w = h ? w1 : w0;
+            const float p0 = exp2_fast(z0 + n), p1 = exp2_fast(z1 + n);
+            if (h) l1 += p0 + p1; else l0 += p0 + p1;
+            if (FP8) {
+              const __half2 x = __floats2half2_rn(copysignf(exp2_fast(z0 + lv[i][0] + w), vs[i][0]),
+                                                  copysignf(exp2_fast(z1 + lv[i][1] + w), vs[i][1]));
+              pa[2 * i + h] = *reinterpret_cast<const uint32_t *>(&x);
+            } else {
+              pa[2 * i + h] = pack_bf16x2(p0, p1);
+            }
+          }
+        if (R <= 8) pa[1] = pa[3] = 0;
         // matrices: (keys 0-7, dims d), (keys 8-15, dims d), (keys 0-7, dims d + 8), ...
         const int r = lane & 15, h = lane >> 4;
         const uint32_t vrow = (FP8 ? sm + C::NST * C::STAGE : vb) + r * 256;
 #pragma unroll
         for (int d = 0; d < 16; d += 2) {
           uint32_t b[4];
-          ldsm4_t(b, vrow + (((d + h) ^ (r & 7)) << 4));
-          mma_bf16(o[d], pa, b[0], b[1]);
-          mma_bf16(o[d + 1], pa, b[2], b[3]);
+          if (FP8) {
+            ldsm4_t(b, vrow + (((d >> 1) ^ (r & 7)) << 4) + h * 128);
+            mma_f16(o[d], pa, b[0], b[1]);
+            mma_f16(o[d + 1], pa, b[2], b[3]);
+          } else {
+            ldsm4_t(b, vrow + (((d + h) ^ (r & 7)) << 4));
+            mma_bf16(o[d], pa, b[0], b[1]);
+            mma_bf16(o[d + 1], pa, b[2], b[3]);
+          }
         }
       }
       __syncwarp();
@@ -600,8 +647,10 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
           M0 = fmaxf(M0, s_m[w * 16 + g4]);
           M1 = fmaxf(M1, s_m[w * 16 + g4 + 8]);
         }
-        const float f0 = m0 == -INFINITY ? 0.f : exp2_fast((m0 - M0) * a.scale_log2);
-        const float f1 = m1 == -INFINITY ? 0.f : exp2_fast((m1 - M1) * a.scale_log2);
+        // O's unit, 2^(scale m) (8-bit: 2^mw), to 2^(scale M)
+        const float u0 = FP8 ? mw0 : m0 * a.scale_log2, u1 = FP8 ? mw1 : m1 * a.scale_log2;
+        const float f0 = u0 == -INFINITY ? 0.f : exp2_fast(u0 - M0 * a.scale_log2);
+        const float f1 = u1 == -INFINITY ? 0.f : exp2_fast(u1 - M1 * a.scale_log2);
         // warp by warp, so that the sum's order is always the same
         for (int w = 0; w < 4; ++w) {
           if (w == warp) {
@@ -633,7 +682,7 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
             L += s_m[w * 16 + r] == -INFINITY ? 0.f : s_l[w * 16 + r] * exp2_fast((s_m[w * 16 + r] - M) * a.scale_log2);
           const float x = s_o[r * kHeadDim + tid];
           if (whole) {
-            const size_t orow = size_t(cu.b) * a.H + cu.g * R + r;
+            const size_t orow = size_t(cu.b) * a.H + g * R + r;
             reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + tid] = __float2bfloat16(L > 0.f ? x / L : 0.f);
             if (tid == 0 && a.lse) a.lse[orow] = L > 0.f ? M * a.scale + logf(L) : -INFINITY;
           } else {
@@ -642,12 +691,12 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
           }
         }
         if (!done && !head) {
-          // the pair ends with tile u + pair_left; the CTA whose run holds that
+          // the pair ends with tile u + pair_left: parts up to the group whose run holds that
           const long long e = u + 1 + pair_left;
-          meta = make_int4(cu.b, cu.g, int((e * n_cta + T - 1) / T - 1), 0);
+          meta = make_int4(cu.b, g, int((e * n_grp + T - 1) / T - 1) - grp + 1, 0);
         }
         __syncthreads();   // s_o, s_m and s_l are free again
-        m0 = m1 = -INFINITY;
+        m0 = m1 = mw0 = mw1 = -INFINITY;
         l0 = l1 = 0.f;
 #pragma unroll
         for (int d = 0; d < 16; ++d)
@@ -674,7 +723,8 @@ __global__ void __launch_bounds__(kPdThreads, 2) paged_decode_kernel(const Paged
 }
 
 // Joins the parts of the pair that CTA blockIdx.x of the decode left
-// unfinished (its slot 1, then slot 0 of the following CTAs), for one head:
+// unfinished (its slot 1, then slot 0 of the following groups' CTAs of the
+// same KV head), for one head:
 // out = sum_p 2^(s (M_p - M)) O_p / sum_p 2^(s (M_p - M)) L_p.
 __global__ void __launch_bounds__(512) paged_join_kernel(const PagedDecodeArgs a, int R) {
   __shared__ float s_x[4][kHeadDim], s_l[4], s_max[16];
@@ -682,8 +732,8 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const PagedDecodeArgs a
   const int cta = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const int4 meta = a.meta[cta];
   if (meta.x < 0) return;
-  const int n = meta.z - cta + 1;
-  auto part = [&](int p) { return a.parts + (size_t(p == 0 ? 2 * cta + 1 : 2 * (cta + p)) * R + r) * kPdRow; };
+  const int n = meta.z;
+  auto part = [&](int p) { return a.parts + (size_t(p == 0 ? 2 * cta + 1 : 2 * (cta + p * a.G)) * R + r) * kPdRow; };
   float M = -INFINITY;
   for (int p = tid; p < n; p += 512) M = fmaxf(M, __ldcg(part(p) + kHeadDim));
 #pragma unroll
@@ -719,10 +769,14 @@ cudaError_t launch_decode_rt(const PagedDecodeArgs &a, int num_sms, cudaStream_t
   auto kern = paged_decode_kernel<R, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // no more CTAs than tiles there can be (Lmax tokens in each sequence)
-  const long long most = (long long)a.B * a.G * ((a.Lmax + kPdTile - 1) / kPdTile);
-  int grid = 2 * num_sms < kPdMaxGrid ? 2 * num_sms : kPdMaxGrid;
-  if (most < grid) grid = most > 0 ? int(most) : 1;
+  // groups of one CTA per KV head: as many as are resident at once, no more
+  // than there can be tiles (Lmax tokens in each sequence)
+  const long long most = (long long)a.B * ((a.Lmax + kPdTile - 1) / kPdTile);
+  long long groups = PdCfg<R, FP8>::CTAS * num_sms / a.G;
+  if (groups > kPdMaxGrid / a.G) groups = kPdMaxGrid / a.G;
+  if (groups > most) groups = most;
+  if (groups < 1) groups = 1;
+  const int grid = int(groups) * a.G;
   kern<<<grid, kPdThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
