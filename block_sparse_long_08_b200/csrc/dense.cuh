@@ -7,8 +7,9 @@
 
 namespace msa {
 
-// Checks cu_q and cu_k, writes seqs, items and n_items (see DenseArgs).
-cudaError_t launch_dense_plan(const DenseArgs &a, cudaStream_t st);
+// Checks cu_q and cu_k, writes seqs, the list of items of `per` queries and,
+// when a.items_k is given, that of key tiles (see DenseArgs).
+cudaError_t launch_dense_plan(const DenseArgs &a, int per, cudaStream_t st);
 
 // Programmatic dependent launch: wait for the kernel before this one in the
 // stream, and let the next one start its own prologue.

@@ -1,106 +1,685 @@
 // Backward pass of dense causal attention over packed sequences.
 //   P = exp(scale q.k - lse), dP = dout . v, D = dout . out, dZ = P (dP - D)
 //   dq = scale sum dZ k,  dk += scale dZ q,  dv += P dout.
+//
+//   dense_stat_kernel  {-lse log2 e, -D} of every (query row, head).
+//   dense_dkv_kernel   key tiles outer: one work item is 128 keys of a KV
+//                 head and every 128-row query tile (128/R queries x R heads)
+//                 that sees one of them.  Transposed products, so that what
+//                 the softmax makes is the A operand from TMEM:
+//                   S^T = K Q^T, dP^T = V dO^T   (TMEM lanes are keys)
+//                   dV += P^T dO, dK += dZ^T Q   (P^T, dZ^T over S^T, dP^T)
+//   dense_dq_kernel    query tiles outer: one item is a 128-row query tile:
+//                   S = Q K^T, dP = dO V^T, dQ += dZ K  (dZ over S).
+//
+// S and dP are computed in both kernels: 7 products where one kernel with
+// atomics on dq would need 5.  In return no gradient is summed by atomics (the
+// result repeats bit for bit) and nothing of dq's size is kept in fp32.
+// Roles in both kernels (one persistent CTA per SM, three warpgroups): warp 0
+// loads by TMA, warp 1 issues UMMAs, warps 2-3 help, warps 4-11 are the
+// softmax: two warpgroups, one TMEM lane per thread, 64 of the 128 columns
+// each; each writes its bf16 results over its own half of what it read.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "dense.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace msa {
 
 namespace {
 
-// The sequence that owns packed row r (by the starts in seqs[].x or, for
-// keys, seqs[].z): the last with start <= r.  False when r lies in none.
-template <bool KEY>
-__device__ __forceinline__ bool find_seq(const DenseArgs &a, int r, int4 &s) {
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((KEY ? a.seqs[mid].z : a.seqs[mid].x) <= r) lo = mid; else hi = mid - 1;
-  }
-  s = a.seqs[lo];
-  return KEY ? (r >= s.z && r < s.z + s.w) : (r >= s.x && r < s.x + s.y);
+constexpr int kBThreads = 384;
+constexpr int kBTile = 32768;                       // 128 rows x 256 B
+// Six tiles: two that stay for an item, two stages of two that stream.
+constexpr int kBSKeep = 0, kBSRing = 2 * kBTile, kBCtl = 6 * kBTile;
+constexpr int kBRegsRest = 72, kBRegsSoftmax = 216;   // 128 * 72 + 256 * 216 = 384 * 168
+constexpr uint32_t kBDescHi = sdesc_hi(1024);
+
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ float4 row4(const uint16_t *p, size_t row, int lane) {
-  const uint2 w = reinterpret_cast<const uint2 *>(p + row * kHeadDim)[lane];
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
-__device__ __forceinline__ float dot4(const float4 &x, const float4 &y) {
-  float z = x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+// D (+)= A B^T over 128 elements of the head dim, both operands K-major tiles.
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a_lo, uint32_t b_lo) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  return z;
-}
-__device__ __forceinline__ void axpy4(float4 &y, float a, const float4 &x) {
-  y.x = fmaf(a, x.x, y.x);
-  y.y = fmaf(a, x.y, y.y);
-  y.z = fmaf(a, x.z, y.z);
-  y.w = fmaf(a, x.w, y.w);
-}
-__device__ __forceinline__ void put_row4(uint16_t *p, size_t row, int lane, const float4 &x, float f) {
-  reinterpret_cast<uint2 *>(p + row * kHeadDim)[lane] =
-      make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-}
-
-// dq: one warp per (query row, head).
-__global__ void __launch_bounds__(256) dense_bwd_dq_kernel(const DenseArgs a) {
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int r = int(w / a.H), h = int(w % a.H), g = h / (a.H / a.G);
-  int4 s;
-  if (r >= a.nq || !find_seq<false>(a, r, s)) return;
-  const int n_vis = s.w - s.y + (r - s.x) + 1;
-  const float4 q = row4(a.q, size_t(w), lane), go = row4(a.dout, size_t(w), lane);
-  const float D = dot4(go, row4(a.out, size_t(w), lane));
-  const float lse2 = a.lse[w] * 1.4426950408889634f;
-  float4 dq = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = 0; x < n_vis; ++x) {
-    const size_t kr = size_t(s.z + x) * a.G + g;
-    const float4 k = row4(a.k, kr, lane);
-    const float p = exp2f(dot4(q, k) * a.scale_log2 - lse2);
-    axpy4(dq, p * (dot4(go, row4(a.v, kr, lane)) - D), k);
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+    umma_f16_ss_w(d, a_lo + off, kBDescHi, b_lo + off, kBDescHi, idesc, kk > 0);
   }
-  put_row4(a.dq, size_t(w), lane, dq, a.scale);
+}
+// D (+)= A B: A from TMEM (bf16 pairs, the first 64 of the 128 summed-over
+// indices at `a`, the others at a + 64), B a tile whose rows are summed over.
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint32_t b_lo, bool add) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 1);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    umma_f16_ts_w(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b_lo + ((kk * 2048) >> 4), kBDescHi, idesc,
+                  add || kk > 0);
 }
 
-// dk, dv: one warp per (key row, KV head), over the query rows that see it.
-__global__ void __launch_bounds__(256) dense_bwd_dkv_kernel(const DenseArgs a) {
+__device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
+  float t0[32], t1[32];
+  tmem_ld32(taddr, t0);
+  tmem_ld32(taddr + 32, t1);
+  tmem_wait_ld();
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    v[c] = t0[c];
+    v[32 + c] = t1[c];
+  }
+}
+// 64 values as bf16 pairs into 32 columns.
+__device__ __forceinline__ void store64(uint32_t taddr, const float (&v)[64]) {
+  uint32_t w[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  tmem_st32u(taddr, w);
+  tmem_wait_st();
+}
+// 64 values times f as bf16 into one row's 128 bytes.
+__device__ __forceinline__ void put64(uint16_t *dst, const float (&v)[64], float f) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    reinterpret_cast<uint4 *>(dst)[c] =
+        make_uint4(pack_bf16x2(v[8 * c] * f, v[8 * c + 1] * f), pack_bf16x2(v[8 * c + 2] * f, v[8 * c + 3] * f),
+                   pack_bf16x2(v[8 * c + 4] * f, v[8 * c + 5] * f), pack_bf16x2(v[8 * c + 6] * f, v[8 * c + 7] * f));
+}
+__device__ __forceinline__ void load_tile(uint32_t dst, const void *tm, uint32_t bar, int y, int z) {
+  tma_load_3d(dst, tm, bar, 0, y, z);
+  tma_load_3d(dst + 16384, tm, bar, 64, y, z);
+}
+// Rows [row0, 128) of a tile to zero (one or two warps, thread `t` of `n`).
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int row0, int t, int n) {
+  for (int i = row0 * 8 + t; i < 1024; i += n) {
+    *reinterpret_cast<uint4 *>(tile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4 *>(tile + 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+// This CTA's work item in round r (snake order), or -1.
+__device__ __forceinline__ int round_item(int r, int n_work) {
+  const int u = r * gridDim.x + ((r & 1) ? (gridDim.x - 1 - blockIdx.x) : blockIdx.x);
+  return u < n_work ? u : -1;
+}
+
+// ------------------------------------------------------------------ statistics
+__global__ void __launch_bounds__(256) dense_stat_kernel(const DenseArgs a) {
   const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int r = int(w / a.G), g = int(w % a.G), R = a.H / a.G;
-  int4 s;
-  if (r >= a.nk || !find_seq<true>(a, r, s)) return;
-  const float4 k = row4(a.k, size_t(w), lane), v = row4(a.v, size_t(w), lane);
-  float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
-  // query i sees key x = r - s.z when x <= nk - nq + i
-  for (int i = max(0, (r - s.z) - (s.w - s.y)); i < s.y; ++i)
-    for (int h = g * R; h < (g + 1) * R; ++h) {
-      const size_t qr = size_t(s.x + i) * a.H + h;
-      const float4 q = row4(a.q, qr, lane), go = row4(a.dout, qr, lane);
-      const float D = dot4(go, row4(a.out, qr, lane));
-      const float p = exp2f(dot4(q, k) * a.scale_log2 - a.lse[qr] * 1.4426950408889634f);
-      axpy4(dv, p, go);
-      axpy4(dk, p * (dot4(go, v) - D), q);
-    }
-  put_row4(a.dk, size_t(w), lane, dk, a.scale);
-  put_row4(a.dv, size_t(w), lane, dv, 1.f);
+  if (w >= (long long)a.nq * a.H) return;
+  const uint2 x = reinterpret_cast<const uint2 *>(a.out + w * kHeadDim)[lane];
+  const uint2 y = reinterpret_cast<const uint2 *>(a.dout + w * kHeadDim)[lane];
+  float s = bf16_lo(x.x) * bf16_lo(y.x);
+  s = fmaf(bf16_hi(x.x), bf16_hi(y.x), s);
+  s = fmaf(bf16_lo(x.y), bf16_lo(y.y), s);
+  s = fmaf(bf16_hi(x.y), bf16_hi(y.y), s);
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  if (lane == 0) a.stat[w] = make_float2(-a.lse[w] * 1.4426950408889634f, -s);
 }
 
-unsigned warps_grid(long long warps) { return unsigned((warps + 7) / 8); }
+// ------------------------------------------------------------------ dk, dv
+struct KvItem {
+  int g, key0, keys;      // first packed key row, keys of the tile that exist
+  int q0, n, qt0, n_qt;   // the sequence's first query row and queries; its query tiles that see the tile
+  int rel;                // key (of the tile) that query 0 sees last: 128 kt - off subtracted
+};
+template <int R>
+__device__ __forceinline__ bool kv_item(const DenseArgs &a, int r, int n_work, KvItem &w) {
+  constexpr int QPI = 128 / R;
+  const int u = round_item(r, n_work);
+  if (u < 0) return false;
+  const int2 it = a.items_k[u / a.G];
+  const int4 s = a.seqs[it.x];
+  w.g = u % a.G;
+  w.key0 = s.z + it.y * 128;
+  w.keys = min(128, s.w - it.y * 128);
+  w.q0 = s.x;
+  w.n = s.y;
+  w.rel = s.w - s.y - it.y * 128;              // query i sees keys 0 .. rel + i of the tile
+  const int first = max(0, -w.rel);             // first query that sees a key of the tile
+  w.qt0 = first / QPI;
+  w.n_qt = first < s.y ? (s.y + QPI - 1) / QPI - w.qt0 : 0;
+  return true;
+}
+
+// barriers
+constexpr int kVKvFull = 0, kVKvEmpty = 1, kVQFull = 2, kVQEmpty = 4, kVStFull = 6, kVStEmpty = 8,
+              kVSFull = 10, kVDpFull = 11, kVPFull = 12, kVZFull = 13, kVAccFull = 14, kVAccEmpty = 15,
+              kVDrain = 16, kVNumBars = 17;
+constexpr int kVMisc = kVNumBars * 8;                // tmem holder, abort flag
+constexpr int kVStat = (kVMisc + 8 + 15) & ~15;      // [2 stages][128] -lse log2 e, [2][128] -D
+constexpr int kVSmem = kBCtl + kVStat + 4 * 128 * 4 + 1024;
+static_assert(kVSmem <= 232448, "shared memory budget");
+constexpr uint32_t kVTmS = 0, kVTmDP = 128, kVTmDV = 256, kVTmDK = 384;
+
+// The softmax and the UMMAs take turns on the two halves of TMEM's working
+// columns: while the softmax makes P of tile i, dK += dZ Q of tile i-1 and dP
+// of tile i run; while it makes dZ of tile i, dV += P dO and S of tile i+1.
+template <int R>
+__global__ void __launch_bounds__(kBThreads, 1)
+    dense_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const DenseArgs a) {
+  constexpr int QPI = 128 / R;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_base = smem_u32(smem);
+  uint8_t *ctl = smem + kBCtl;
+  const uint32_t bar0 = smem_u32(ctl);
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ctl + kVMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(ctl + kVMisc + 4);
+  float *s_nl = reinterpret_cast<float *>(ctl + kVStat), *s_nd = s_nl + 256;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kVNumBars; ++i)
+      mbar_init(bar(i), i == kVStFull || i == kVStFull + 1 ? 64
+                        : (i == kVStEmpty || i == kVStEmpty + 1 || i == kVPFull || i == kVZFull || i == kVAccEmpty)
+                            ? 256
+                            : 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tmem_holder;
+  const int n_work = *a.n_items_k * a.G;
+  KvItem w;
+
+  if (warp < 4) {
+    regs_dec<kBRegsRest>();
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------- TMA producer
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_do);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      uint32_t it = 0, seq = 0;
+      bool ok = true;
+      for (int r = 0; ok && kv_item<R>(a, r, n_work, w); ++r) {
+        if (w.n_qt == 0) continue;
+        ok = mbar_wait(bar(kVKvEmpty), (it & 1) ^ 1, abort_flag, a.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bar(kVKvFull), 2 * kBTile);
+        load_tile(s_base + kBSKeep, &tm_k, bar(kVKvFull), w.g, w.key0);
+        load_tile(s_base + kBSKeep + kBTile, &tm_v, bar(kVKvFull), w.g, w.key0);
+        ++it;
+        for (int i = 0; i < w.n_qt && ok; ++i) {
+          const int st = seq & 1;
+          ok = mbar_wait(bar(kVQEmpty + st), ((seq >> 1) & 1) ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(kVQFull + st), 2 * kBTile);
+          const int row = w.q0 + (w.qt0 + i) * QPI;
+          load_tile(s_base + kBSRing + st * 2 * kBTile, &tm_q, bar(kVQFull + st), w.g * R, row);
+          load_tile(s_base + kBSRing + st * 2 * kBTile + kBTile, &tm_do, bar(kVQFull + st), w.g * R, row);
+          ++seq;
+        }
+      }
+      // copies still in flight land before the CTA may exit
+      if (it) mbar_wait_drain(bar(kVKvFull), (it - 1) & 1);
+      for (uint32_t x = 1; x <= 2; ++x)
+        if (seq >= x) mbar_wait_drain(bar(kVQFull + ((seq - x) & 1)), ((seq - x) >> 1) & 1);
+    } else if (warp == 1 && lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      const uint32_t k_lo = sdesc_lo(s_base + kBSKeep, 16), v_lo = sdesc_lo(s_base + kBSKeep + kBTile, 16);
+      const uint32_t qk_lo = sdesc_lo(s_base + kBSRing, 16), qm_lo = sdesc_lo(s_base + kBSRing, 16384);
+      constexpr uint32_t T = kBTile >> 4;
+      uint32_t it = 0, seq = 0;
+      bool ok = true;
+      for (int r = 0; ok && kv_item<R>(a, r, n_work, w); ++r) {
+        if (w.n_qt == 0) continue;
+        ok = mbar_wait(bar(kVKvFull), it & 1, abort_flag, a.status) &&
+             mbar_wait(bar(kVQFull + (seq & 1)), (seq >> 1) & 1, abort_flag, a.status);
+        if (!ok) break;
+        mma_tiles(tm + kVTmS, k_lo, qk_lo + (seq & 1) * 2 * T);
+        umma_commit(bar(kVSFull));
+        mma_tiles(tm + kVTmDP, v_lo, qk_lo + (seq & 1) * 2 * T + T);
+        umma_commit(bar(kVDpFull));
+        ok = mbar_wait(bar(kVAccEmpty), (it & 1) ^ 1, abort_flag, a.status);
+        for (int i = 0; i < w.n_qt && ok; ++i, ++seq) {
+          const uint32_t st = seq & 1, nx = (seq + 1) & 1;
+          const bool more = i + 1 < w.n_qt;
+          if (more) ok = mbar_wait(bar(kVQFull + nx), ((seq + 1) >> 1) & 1, abort_flag, a.status);
+          ok = ok && mbar_wait(bar(kVPFull), seq & 1, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          mma_from_tmem(tm + kVTmDV, tm + kVTmS, qm_lo + st * 2 * T + T, i > 0);
+          if (more) {
+            mma_tiles(tm + kVTmS, k_lo, qk_lo + nx * 2 * T);
+            umma_commit(bar(kVSFull));
+          }
+          ok = mbar_wait(bar(kVZFull), seq & 1, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          mma_from_tmem(tm + kVTmDK, tm + kVTmDP, qm_lo + st * 2 * T, i > 0);
+          umma_commit(bar(kVQEmpty + st));
+          if (more) {
+            mma_tiles(tm + kVTmDP, v_lo, qk_lo + nx * 2 * T + T);
+            umma_commit(bar(kVDpFull));
+          }
+        }
+        if (!ok) break;
+        umma_commit(bar(kVAccFull));
+        umma_commit(bar(kVKvEmpty));
+        ++it;
+      }
+      umma_commit(bar(kVDrain));
+      mbar_wait_drain(bar(kVDrain), 0);
+    } else if (warp >= 2) {
+      // -------------------------------------------------------- helpers
+      // each query tile's statistics; and in a sequence's last tile the rows
+      // behind its last query, which belong to others: their P and dZ are 0,
+      // but 0 times a NaN there would not be
+      const int ht = tid - 64;
+      uint32_t seq = 0;
+      bool ok = true;
+      for (int r = 0; ok && kv_item<R>(a, r, n_work, w); ++r) {
+        for (int i = 0; i < w.n_qt; ++i, ++seq) {
+          const int st = seq & 1, qa = (w.qt0 + i) * QPI;
+          ok = mbar_wait(bar(kVStEmpty + st), ((seq >> 1) & 1) ^ 1, abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+#pragma unroll
+          for (int x = ht; x < 128; x += 64) {
+            const int qi = qa + x / R;
+            const float2 v = qi < w.n ? a.stat[size_t(w.q0 + qi) * a.H + w.g * R + x % R] : make_float2(0.f, 0.f);
+            s_nl[st * 128 + x] = v.x;
+            s_nd[st * 128 + x] = v.y;
+          }
+          if (w.n - qa < QPI) {
+            ok = mbar_wait(bar(kVQFull + st), (seq >> 1) & 1, abort_flag, a.status);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            uint8_t *tile = smem + kBSRing + st * 2 * kBTile;
+            clear_rows(tile, (w.n - qa) * R, ht, 64);
+            clear_rows(tile + kBTile, (w.n - qa) * R, ht, 64);
+            fence_proxy_async_smem();
+          }
+          mbar_arrive(bar(kVStFull + st));
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    regs_inc<kBRegsSoftmax>();
+    const int hc = (warp - 4) >> 2;                  // query rows 64 hc .. of each tile
+    const int key = (warp & 3) * 32 + lane;          // TMEM lane
+    const uint32_t tl = tm + (uint32_t((warp & 3) * 32) << 16);
+    const float2 sc2 = f2_dup(a.scale_log2);
+    uint32_t seq = 0, it = 0;
+    bool ok = true;
+    for (int r = 0; ok && kv_item<R>(a, r, n_work, w); ++r) {
+      const size_t grow = size_t(w.key0 + key) * a.G + w.g;
+      uint16_t *dk = a.dk + grow * kHeadDim + hc * 64, *dv = a.dv + grow * kHeadDim + hc * 64;
+      if (w.n_qt == 0) {                             // no query sees a key of the tile
+        if (key < w.keys) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            reinterpret_cast<uint4 *>(dk)[c] = reinterpret_cast<uint4 *>(dv)[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      for (int i = 0; i < w.n_qt; ++i, ++seq) {
+        const int st = seq & 1, qa = (w.qt0 + i) * QPI;
+        ok = mbar_wait(bar(kVStFull + st), (seq >> 1) & 1, abort_flag, a.status) &&
+             mbar_wait(bar(kVSFull), seq & 1, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        float p[64];
+        load64(tl + kVTmS + hc * 64, p);
+        // rows that see this key: query qa + row / R >= key - rel, up to the last query
+        const int lo = (key - w.rel - qa) * R - hc * 64, hi = (w.n - qa) * R - hc * 64;
+        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
+        const float4 *nl = reinterpret_cast<const float4 *>(s_nl + st * 128 + hc * 64);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 x = nl[c];
+          const float2 z0 = f2_fma(make_float2(p[4 * c], p[4 * c + 1]), sc2, make_float2(x.x, x.y));
+          const float2 z1 = f2_fma(make_float2(p[4 * c + 2], p[4 * c + 3]), sc2, make_float2(x.z, x.w));
+          p[4 * c] = fast_exp2(z0.x);
+          p[4 * c + 1] = fast_exp2(z0.y);
+          p[4 * c + 2] = fast_exp2(z1.x);
+          p[4 * c + 3] = fast_exp2(z1.y);
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
+        }
+        store64(tl + kVTmS + hc * 64, p);
+        tc_fence_before();
+        mbar_arrive(bar(kVPFull));
+        ok = mbar_wait(bar(kVDpFull), seq & 1, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        float z[64];
+        load64(tl + kVTmDP + hc * 64, z);
+        const float4 *nd = reinterpret_cast<const float4 *>(s_nd + st * 128 + hc * 64);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 x = nd[c];
+          const float2 z0 = f2_mul(f2_add(make_float2(z[4 * c], z[4 * c + 1]), make_float2(x.x, x.y)),
+                                   make_float2(p[4 * c], p[4 * c + 1]));
+          const float2 z1 = f2_mul(f2_add(make_float2(z[4 * c + 2], z[4 * c + 3]), make_float2(x.z, x.w)),
+                                   make_float2(p[4 * c + 2], p[4 * c + 3]));
+          z[4 * c] = z0.x; z[4 * c + 1] = z0.y;
+          z[4 * c + 2] = z1.x; z[4 * c + 3] = z1.y;
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) z[c] = (c >= lo && c < hi) ? z[c] : 0.f;
+        }
+        store64(tl + kVTmDP + hc * 64, z);
+        tc_fence_before();
+        mbar_arrive(bar(kVZFull));
+        mbar_arrive(bar(kVStEmpty + st));
+      }
+      if (!ok) break;
+      ok = mbar_wait(bar(kVAccFull), it & 1, abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++it;
+      tc_fence_after();
+      float x[64];
+      load64(tl + kVTmDV + hc * 64, x);
+      if (key < w.keys) put64(dv, x, 1.f);
+      load64(tl + kVTmDK + hc * 64, x);
+      tc_fence_before();
+      mbar_arrive(bar(kVAccEmpty));
+      if (key < w.keys) put64(dk, x, a.scale);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dq
+struct QItem {
+  int g, q0, n, hi0, key0, m, n_kt;   // first packed query row, queries of the tile, last key of the first
+};
+template <int R>
+__device__ __forceinline__ bool q_item(const DenseArgs &a, int r, int n_work, QItem &w) {
+  constexpr int QPI = 128 / R;
+  const int u = round_item(r, n_work);
+  if (u < 0) return false;
+  const int2 it = a.items[u / a.G];
+  const int4 s = a.seqs[it.x];
+  w.g = u % a.G;
+  w.q0 = s.x + it.y * QPI;
+  w.n = min(QPI, s.y - it.y * QPI);
+  w.hi0 = s.w - s.y + it.y * QPI;
+  w.key0 = s.z;
+  w.m = s.w;
+  const int last = w.hi0 + w.n - 1;
+  w.n_kt = last >= 0 ? (last >> 7) + 1 : 0;
+  return true;
+}
+
+constexpr int kGQFull = 0, kGQEmpty = 1, kGKvFull = 2, kGKvEmpty = 4, kGSFull = 6, kGDpFull = 8, kGZFull = 9,
+              kGAccFull = 10, kGAccEmpty = 11, kGReq = 12, kGClean = 13, kGDrain = 14, kGNumBars = 15;
+constexpr int kGMisc = kGNumBars * 8;
+constexpr int kGSmem = kBCtl + kGMisc + 16 + 1024;
+static_assert(kGSmem <= 232448, "shared memory budget");
+constexpr uint32_t kGTmS = 0, kGTmDP = 256, kGTmDQ = 384;   // S: two buffers of 128 columns
+
+// S of key tile j+1 runs under the softmax of tile j; dP of tile j+1 and
+// dQ += dZ K of tile j under the exponentials of tile j+1.
+template <int R>
+__global__ void __launch_bounds__(kBThreads, 1)
+    dense_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const DenseArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s_base = smem_u32(smem);
+  uint8_t *ctl = smem + kBCtl;
+  const uint32_t bar0 = smem_u32(ctl);
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ctl + kGMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(ctl + kGMisc + 4);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kGNumBars; ++i) mbar_init(bar(i), (i == kGZFull || i == kGAccEmpty) ? 256 : 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tmem_holder;
+  const int n_work = *a.n_items * a.G;
+  QItem w;
+
+  if (warp < 4) {
+    regs_dec<kBRegsRest>();
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------- TMA producer
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_do);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      uint32_t it = 0, seq = 0;
+      bool ok = true;
+      for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+        if (w.n_kt == 0) continue;
+        ok = mbar_wait(bar(kGQEmpty), (it & 1) ^ 1, abort_flag, a.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bar(kGQFull), 2 * kBTile);
+        load_tile(s_base + kBSKeep, &tm_q, bar(kGQFull), w.g * R, w.q0);
+        load_tile(s_base + kBSKeep + kBTile, &tm_do, bar(kGQFull), w.g * R, w.q0);
+        ++it;
+        for (int j = 0; j < w.n_kt && ok; ++j) {
+          const int st = seq & 1;
+          ok = mbar_wait(bar(kGKvEmpty + st), ((seq >> 1) & 1) ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(kGKvFull + st), 2 * kBTile);
+          load_tile(s_base + kBSRing + st * 2 * kBTile, &tm_k, bar(kGKvFull + st), w.g, w.key0 + j * 128);
+          load_tile(s_base + kBSRing + st * 2 * kBTile + kBTile, &tm_v, bar(kGKvFull + st), w.g, w.key0 + j * 128);
+          ++seq;
+        }
+      }
+      if (it) mbar_wait_drain(bar(kGQFull), (it - 1) & 1);
+      for (uint32_t x = 1; x <= 2; ++x)
+        if (seq >= x) mbar_wait_drain(bar(kGKvFull + ((seq - x) & 1)), ((seq - x) >> 1) & 1);
+    } else if (warp == 1 && lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      const uint32_t q_lo = sdesc_lo(s_base + kBSKeep, 16), do_lo = sdesc_lo(s_base + kBSKeep + kBTile, 16);
+      const uint32_t kk_lo = sdesc_lo(s_base + kBSRing, 16), km_lo = sdesc_lo(s_base + kBSRing, 16384);
+      constexpr uint32_t T = kBTile >> 4;
+      uint32_t it = 0, seq = 0, cn = 0;
+      bool ok = true;
+      for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+        if (w.n_kt == 0) continue;
+        ok = mbar_wait(bar(kGQFull), it & 1, abort_flag, a.status) &&
+             mbar_wait(bar(kGKvFull + (seq & 1)), (seq >> 1) & 1, abort_flag, a.status);
+        if (!ok) break;
+        mma_tiles(tm + kGTmS + (seq & 1) * 128, q_lo, kk_lo + (seq & 1) * 2 * T);
+        umma_commit(bar(kGSFull + (seq & 1)));
+        mma_tiles(tm + kGTmDP, do_lo, kk_lo + (seq & 1) * 2 * T + T);
+        umma_commit(bar(kGDpFull));
+        ok = mbar_wait(bar(kGAccEmpty), (it & 1) ^ 1, abort_flag, a.status);
+        for (int j = 0; j < w.n_kt && ok; ++j, ++seq) {
+          const uint32_t st = seq & 1, nx = (seq + 1) & 1;
+          const bool more = j + 1 < w.n_kt;
+          if (more) {
+            ok = mbar_wait(bar(kGKvFull + nx), ((seq + 1) >> 1) & 1, abort_flag, a.status);
+            if (!ok) break;
+            mma_tiles(tm + kGTmS + nx * 128, q_lo, kk_lo + nx * 2 * T);
+            umma_commit(bar(kGSFull + nx));
+          } else if (w.m - j * 128 < 128) {   // K's rows behind the last key are cleared
+            mbar_arrive(bar(kGReq));
+            ok = mbar_wait(bar(kGClean), cn & 1, abort_flag, a.status);
+            ++cn;
+          }
+          ok = ok && mbar_wait(bar(kGZFull), seq & 1, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (more) {
+            mma_tiles(tm + kGTmDP, do_lo, kk_lo + nx * 2 * T + T);
+            umma_commit(bar(kGDpFull));
+          }
+          mma_from_tmem(tm + kGTmDQ, tm + kGTmS + st * 128, km_lo + st * 2 * T, j > 0);
+          umma_commit(bar(kGKvEmpty + st));
+        }
+        if (!ok) break;
+        umma_commit(bar(kGAccFull));
+        umma_commit(bar(kGQEmpty));
+        ++it;
+      }
+      umma_commit(bar(kGDrain));
+      mbar_wait_drain(bar(kGDrain), 0);
+    } else if (warp == 2) {
+      // -------------------------------------------------------- K cleaner
+      // (dZ of the keys behind the last is 0, but 0 times a NaN would not
+      // be).  The issuer asks when the item's last tile has landed and the
+      // score products that read it are issued or done.
+      uint32_t seq = 0, cn = 0;
+      bool ok = true;
+      for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+        seq += w.n_kt;
+        const int rem = w.m - (w.n_kt - 1) * 128;
+        if (w.n_kt == 0 || rem >= 128) continue;
+        const uint32_t last = seq - 1;
+        ok = mbar_wait(bar(kGReq), cn & 1, abort_flag, a.status) &&
+             mbar_wait(bar(kGKvFull + (last & 1)), (last >> 1) & 1, abort_flag, a.status);
+        ++cn;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        clear_rows(smem + kBSRing + (last & 1) * 2 * kBTile, rem, lane, 32);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kGClean));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    regs_inc<kBRegsSoftmax>();
+    const int hc = (warp - 4) >> 2;                  // keys 64 hc .. of each tile
+    const int row = (warp & 3) * 32 + lane;          // TMEM lane
+    const uint32_t tl = tm + (uint32_t((warp & 3) * 32) << 16);
+    const int qi = row / R, hh = row % R;
+    const float2 sc2 = f2_dup(a.scale_log2);
+    uint32_t seq = 0, it = 0;
+    bool ok = true;
+    for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+      const bool valid = qi < w.n;
+      const size_t qrow = size_t(w.q0 + qi) * a.H + w.g * R + hh;
+      uint16_t *dq = a.dq + qrow * kHeadDim + hc * 64;
+      if (w.n_kt == 0) {                             // no row of the tile sees a key
+        if (valid) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) reinterpret_cast<uint4 *>(dq)[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      const float2 stt = valid ? a.stat[qrow] : make_float2(0.f, 0.f);
+      const float2 nl2 = f2_dup(stt.x), nd2 = f2_dup(stt.y);
+      for (int j = 0; j < w.n_kt; ++j, ++seq) {
+        const uint32_t ts = tl + kGTmS + (seq & 1) * 128 + hc * 64;
+        ok = mbar_wait(bar(kGSFull + (seq & 1)), (seq >> 1) & 1, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        float p[64];
+        load64(ts, p);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 x = f2_fma(make_float2(p[c], p[c + 1]), sc2, nl2);
+          p[c] = fast_exp2(x.x);
+          p[c + 1] = fast_exp2(x.y);
+        }
+        ok = mbar_wait(bar(kGDpFull), seq & 1, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        float z[64];
+        load64(tl + kGTmDP + hc * 64, z);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float2 x = f2_mul(f2_add(make_float2(z[c], z[c + 1]), nd2), make_float2(p[c], p[c + 1]));
+          z[c] = x.x;
+          z[c + 1] = x.y;
+        }
+        const int lim = (valid ? w.hi0 + qi : -1) - j * 128 - hc * 64;   // last visible column
+        if (__any_sync(0xffffffffu, lim < 63)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) z[c] = c <= lim ? z[c] : 0.f;
+        }
+        store64(ts, z);
+        tc_fence_before();
+        mbar_arrive(bar(kGZFull));
+      }
+      if (!ok) break;
+      ok = mbar_wait(bar(kGAccFull), it & 1, abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++it;
+      tc_fence_after();
+      float x[64];
+      load64(tl + kGTmDQ + hc * 64, x);
+      tc_fence_before();
+      mbar_arrive(bar(kGAccEmpty));
+      if (valid) put64(dq, x, a.scale);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+template <int R>
+cudaError_t launch_bwd_r(const CUtensorMap &tq, const CUtensorMap &tdo, const CUtensorMap &tk,
+                         const CUtensorMap &tv, const DenseArgs &a, int num_sms, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(dense_dkv_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kVSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(dense_dq_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
+  if (e != cudaSuccess) return e;
+  const long long wk = (long long)a.max_items_k * a.G, wq = (long long)a.max_items * a.G;
+  if (a.nk > 0)
+    dense_dkv_kernel<R><<<unsigned(wk < num_sms ? wk : num_sms), kBThreads, kVSmem, st>>>(tq, tdo, tk, tv, a);
+  if (a.nq > 0)
+    dense_dq_kernel<R><<<unsigned(wq < num_sms ? wq : num_sms), kBThreads, kGSmem, st>>>(tq, tdo, tk, tv, a);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
-cudaError_t launch_dense_varlen_backward(const DenseArgs &a, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  cudaError_t e = launch_dense_plan(a, st);
+cudaError_t launch_dense_varlen_backward(const CUtensorMap &tq, const CUtensorMap &tdo, const CUtensorMap &tk,
+                                         const CUtensorMap &tv, const DenseArgs &a, int num_sms,
+                                         cudaStream_t st) {
+  cudaError_t e = launch_dense_plan(a, 128 / (a.H / a.G), st);
   if (e != cudaSuccess) return e;
-  if (a.nq > 0) dense_bwd_dq_kernel<<<warps_grid((long long)a.nq * a.H), 256, 0, st>>>(a);
-  if (a.nk > 0) dense_bwd_dkv_kernel<<<warps_grid((long long)a.nk * a.G), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  if (a.nq > 0) {
+    const long long rows = (long long)a.nq * a.H;
+    dense_stat_kernel<<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  switch (a.H / a.G) {
+    case 1: return launch_bwd_r<1>(tq, tdo, tk, tv, a, num_sms, st);
+    case 2: return launch_bwd_r<2>(tq, tdo, tk, tv, a, num_sms, st);
+    case 4: return launch_bwd_r<4>(tq, tdo, tk, tv, a, num_sms, st);
+    case 8: return launch_bwd_r<8>(tq, tdo, tk, tv, a, num_sms, st);
+    case 16: return launch_bwd_r<16>(tq, tdo, tk, tv, a, num_sms, st);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace msa

@@ -82,10 +82,17 @@ __device__ __forceinline__ int block_exclusive(int v, int *s_warp, int &total) {
   return inc - v + (warp ? s_warp[warp - 1] : 0);
 }
 
-// One CTA.  Items are sorted by their number of key tiles, in at most 1024
-// steps of equal width (a counting sort; the order inside a step does not
-// matter, an item's result depends on nothing but the item).
-__global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int per) {
+// One CTA per list: the items of `per` queries (block 0) and the key tiles of
+// 128 keys (block 1, for the backward).  Items are sorted by their number of
+// key tiles (query tiles of qpi queries), in at most 1024 steps of equal
+// width (a counting sort; the order inside a step does not matter, an item's
+// result depends on nothing but the item).
+__global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int per, int qpi) {
+  const bool keys = blockIdx.x == 1;
+  int *prefix = keys ? a.prefix_k : a.prefix;
+  int2 *items = keys ? a.items_k : a.items;
+  const int max_items = keys ? a.max_items_k : a.max_items;
+  if (keys) per = 128;
   __shared__ int s_warp[32];
   __shared__ int s_bin[kPlanBins];
   const int tid = threadIdx.x;
@@ -94,17 +101,17 @@ __global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int
   for (int b = tid; b < a.B; b += 1024) {
     const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
     bad |= q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk;
-    most = max(most, k1 - k0);
+    most = max(most, keys ? (q1 - q0 + qpi - 1) / qpi : (k1 - k0 + 127) / 128);
   }
   bad = __syncthreads_or(bad);
-  if (bad && tid == 0) atomicCAS(a.status, 0, kStatusBadInput);
+  if (bad && tid == 0 && !keys) atomicCAS(a.status, 0, kStatusBadInput);
   s_bin[tid] = 0;
   // the longest sequence sets the width of a step
   for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   if ((tid & 31) == 0) s_warp[tid >> 5] = most;
   __syncthreads();
   for (int w = 0; w < 32; ++w) most = max(most, s_warp[w]);
-  const int width = ((most + 127) / 128) / kPlanBins + 1;
+  const int width = most / kPlanBins + 1;
   int base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 1024) {
     const int b = b0 + tid;
@@ -116,14 +123,14 @@ __global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int
       s.w = a.cu_k[b + 1] - s.z;
     }
     int total;
-    const int before = block_exclusive(ceil_div(s.y, per), s_warp, total);
+    const int before = block_exclusive(ceil_div(keys ? s.w : s.y, per), s_warp, total);
     if (b < a.B) {
-      a.seqs[b] = s;
-      a.prefix[b] = base + before;
+      if (!keys) a.seqs[b] = s;
+      prefix[b] = base + before;
     }
     base += total;
   }
-  if (tid == 0) *a.n_items = base;
+  if (tid == 0) *(keys ? a.n_items_k : a.n_items) = base;
   __syncthreads();
   __threadfence_block();
   // item x: its sequence (the last b with prefix[b] <= x) and place in it
@@ -131,13 +138,15 @@ __global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int
     int lo = 0, hi = a.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.prefix[mid] <= x) lo = mid; else hi = mid - 1;
+      if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
     }
-    const int4 s = a.seqs[lo];
-    const int qt = x - a.prefix[lo];
-    const int seen = s.w - s.y + min(s.y, (qt + 1) * per);   // keys of the item's last row
-    bin = kPlanBins - 1 - min(kPlanBins - 1, max(0, (seen + 127) / 128) / width);
-    return make_int2(lo, qt);
+    const int n = a.cu_q[lo + 1] - a.cu_q[lo], m = a.cu_k[lo + 1] - a.cu_k[lo];
+    const int at = x - prefix[lo];
+    // queries that see the key tile, in tiles; or keys of the item's last row, in tiles
+    const int cost = keys ? (n - max(0, at * 128 - (m - n)) + qpi - 1) / qpi
+                          : (m - n + min(n, (at + 1) * per) + 127) / 128;
+    bin = kPlanBins - 1 - min(kPlanBins - 1, max(0, cost) / width);
+    return make_int2(lo, at);
   };
   for (int x = tid; x < base; x += 1024) {
     int bin;
@@ -154,7 +163,7 @@ __global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int
     int bin;
     const int2 it = item_of(x, bin);
     const int at = atomicAdd(&s_bin[bin], 1);
-    if (at < a.max_items) a.items[at] = it;
+    if (at < max_items) items[at] = it;
   }
 }
 
@@ -593,14 +602,14 @@ cudaError_t launch_fwd_r(const CUtensorMap &tq, const CUtensorMap &tk, const CUt
 
 }  // namespace
 
-cudaError_t launch_dense_plan(const DenseArgs &a, cudaStream_t st) {
-  dense_plan_kernel<<<1, 1024, 0, st>>>(a, dense_item_queries(a.H / a.G));
+cudaError_t launch_dense_plan(const DenseArgs &a, int per, cudaStream_t st) {
+  dense_plan_kernel<<<a.items_k ? 2 : 1, 1024, 0, st>>>(a, per, 128 / (a.H / a.G));
   return cudaGetLastError();
 }
 
 cudaError_t launch_dense_varlen(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                 const DenseArgs &a, int num_sms, cudaStream_t st) {
-  cudaError_t e = launch_dense_plan(a, st);
+  cudaError_t e = launch_dense_plan(a, dense_item_queries(a.H / a.G), st);
   if (e != cudaSuccess) return e;
   switch (a.H / a.G) {
     case 1: return launch_fwd_r<1>(tq, tk, tv, a, num_sms, st);

@@ -258,6 +258,13 @@ struct DenseArgs {
   int2 *items;                 // {sequence, query item}, longest first
   int *n_items;
   int max_items;               // entries of `items`
+  // the backward's: key tiles of 128 keys, most query tiles first, and
+  // {-lse log2 e, -dout . out} of every (query row, head)
+  int *prefix_k;
+  int2 *items_k;
+  int *n_items_k;
+  int max_items_k;
+  float2 *stat;
   uint16_t *out;               // [nq,H,d] (read by the backward)
   float *lse;                  // [nq,H] or null
   const uint16_t *dout;        // backward
@@ -266,9 +273,13 @@ struct DenseArgs {
 };
 // Queries of one forward work item: two 128-row tiles of 128/R queries x R heads.
 inline int dense_item_queries(int R) { return 256 / R; }
+// Entries that a list of items can need: nq / per full ones, and a last one per sequence.
+inline int dense_max_items(int rows, int per, int B) { return rows / per + B; }
 cudaError_t launch_dense_varlen(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                 const DenseArgs &a, int num_sms, cudaStream_t st);
-cudaError_t launch_dense_varlen_backward(const DenseArgs &a, int num_sms, cudaStream_t st);
+cudaError_t launch_dense_varlen_backward(const CUtensorMap &tq, const CUtensorMap &tdo,
+                                         const CUtensorMap &tk, const CUtensorMap &tv,
+                                         const DenseArgs &a, int num_sms, cudaStream_t st);
 
 // Sets the message msa_last_error() returns; returns `code`.
 int report_error(int code, const char *msg);

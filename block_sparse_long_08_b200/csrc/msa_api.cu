@@ -652,22 +652,28 @@ bool dense_op(int op) { return op >= MSA_OP_PAGED_APPEND && op <= MSA_OP_DENSE_V
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Packed-sequence operations: {q0, nq, k0, nk} per sequence, the count and
-// the prefix of its work items, and their list (as many as p->L packed query
-// rows and one more per sequence can make).
+// Packed-sequence operations: {q0, nq, k0, nk} per sequence, the count, the
+// prefix and the list of its work items (as many as p->L packed query rows
+// and one more per sequence can make); for the backward also those of its
+// key tiles, and two floats per (query row, head).
 struct DenseWs {
-  size_t seqs, count, prefix, items, end;
-  int max_items;
+  size_t seqs, count, prefix, items, count_k, prefix_k, items_k, stat, end;
 };
-DenseWs dense_ws(const msa_params *p) {
+DenseWs dense_ws(const msa_params *p, bool backward) {
   DenseWs w;
-  const int per = msa::dense_item_queries(p->H / p->G);
-  w.max_items = p->L / per + p->B;
+  const int r = p->H / p->G, per = backward ? 128 / r : msa::dense_item_queries(r);
   size_t o = msa::kWsHeader;
   w.seqs = o; o = align_up(o + sizeof(int4) * size_t(p->B));
   w.count = o; o = align_up(o + 4);
   w.prefix = o; o = align_up(o + 4 * (size_t(p->B) + 1));
-  w.items = o; o = align_up(o + sizeof(int2) * size_t(w.max_items));
+  w.items = o; o = align_up(o + sizeof(int2) * size_t(msa::dense_max_items(p->L, per, p->B)));
+  w.count_k = w.prefix_k = w.items_k = w.stat = 0;
+  if (backward) {
+    w.count_k = o; o = align_up(o + 4);
+    w.prefix_k = o; o = align_up(o + 4 * (size_t(p->B) + 1));
+    w.items_k = o; o = align_up(o + sizeof(int2) * size_t(msa::dense_max_items(p->L, 128, p->B)));
+    w.stat = o; o = align_up(o + sizeof(float2) * size_t(p->L) * p->H);
+  }
   w.end = o;
   return w;
 }
@@ -687,7 +693,8 @@ PagedDecWs paged_dec_ws(const msa_params *p) {
 
 size_t dense_ws_bytes(const msa_params *p, int op) {
   if (op == MSA_OP_PAGED_DECODE) return paged_dec_ws(p).end;
-  if (op == MSA_OP_DENSE_VARLEN || op == MSA_OP_DENSE_VARLEN_BACKWARD) return dense_ws(p).end;
+  if (op == MSA_OP_DENSE_VARLEN || op == MSA_OP_DENSE_VARLEN_BACKWARD)
+    return dense_ws(p, op == MSA_OP_DENSE_VARLEN_BACKWARD).end;
   return msa::kWsHeader;
 }
 
@@ -740,7 +747,7 @@ int make_packed_kv_tmap(CUtensorMap *m, const void *base, const msa_params *p, i
 // Checks and arguments shared by the packed-sequence forward and backward.
 int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa_bf16 *k,
                const msa_bf16 *v, const int32_t *cu_q, const int32_t *cu_k, const void *out,
-               const float *lse, void *ws, size_t ws_bytes, msa::DenseArgs *a) {
+               const float *lse, bool backward, void *ws, size_t ws_bytes, msa::DenseArgs *a) {
   if (nq < 0 || nk < 0 || nq > p->L || nk > p->L)
     return fail(MSA_ERR_INVALID_ARG, "nq=%d nk=%d: need 0 <= nq, nk <= L=%d", nq, nk, p->L);
   if (!cu_q || !cu_k || (nq > 0 && (!q || !out)) || (nk > 0 && (!k || !v)))
@@ -748,7 +755,7 @@ int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned4(cu_q) ||
       !aligned4(cu_k) || !aligned4(lse))
     return fail(MSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned (cu, lse 4-byte)");
-  const DenseWs w = dense_ws(p);
+  const DenseWs w = dense_ws(p, backward);
   const int rc = check_ws(ws, ws_bytes, w.end);
   if (rc) return rc;
   a->B = p->B; a->H = p->H; a->G = p->G; a->nq = nq; a->nk = nk;
@@ -761,7 +768,17 @@ int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa
   a->n_items = reinterpret_cast<int *>(wsb + w.count);
   a->prefix = reinterpret_cast<int *>(wsb + w.prefix);
   a->items = reinterpret_cast<int2 *>(wsb + w.items);
-  a->max_items = nq / msa::dense_item_queries(p->H / p->G) + p->B;
+  const int r = p->H / p->G;
+  a->max_items = msa::dense_max_items(nq, backward ? 128 / r : msa::dense_item_queries(r), p->B);
+  a->prefix_k = nullptr; a->items_k = nullptr; a->n_items_k = nullptr; a->stat = nullptr;
+  a->max_items_k = 0;
+  if (backward) {
+    a->n_items_k = reinterpret_cast<int *>(wsb + w.count_k);
+    a->prefix_k = reinterpret_cast<int *>(wsb + w.prefix_k);
+    a->items_k = reinterpret_cast<int2 *>(wsb + w.items_k);
+    a->stat = reinterpret_cast<float2 *>(wsb + w.stat);
+    a->max_items_k = msa::dense_max_items(nk, 128, p->B);
+  }
   a->out = nullptr; a->lse = nullptr;
   a->dout = nullptr; a->dq = a->dk = a->dv = nullptr;
   a->status = status_ptr(ws);
@@ -1405,7 +1422,7 @@ int msa_dense_attn_varlen(const msa_params *p, int nq, int nk, const msa_bf16 *q
   if (rc) return rc;
   if (p->B == 0) return MSA_OK;
   msa::DenseArgs a;
-  rc = dense_args(p, nq, nk, q, k, v, cu_q, cu_k, out, lse, ws, ws_bytes, &a);
+  rc = dense_args(p, nq, nk, q, k, v, cu_q, cu_k, out, lse, false, ws, ws_bytes, &a);
   if (rc) return rc;
   if (nq == 0) return MSA_OK;
   a.out = out;
@@ -1431,7 +1448,7 @@ int msa_dense_attn_varlen_backward(const msa_params *p, int nq, int nk, const ms
   if (rc) return rc;
   if (p->B == 0) return MSA_OK;
   msa::DenseArgs a;
-  rc = dense_args(p, nq, nk, q, k, v, cu_q, cu_k, out, lse, ws, ws_bytes, &a);
+  rc = dense_args(p, nq, nk, q, k, v, cu_q, cu_k, out, lse, true, ws, ws_bytes, &a);
   if (rc) return rc;
   if ((nq > 0 && (!lse || !dout || !dq)) || (nk > 0 && (!dk || !dv)))
     return fail(MSA_ERR_INVALID_ARG, "NULL tensor pointer");
@@ -1441,8 +1458,14 @@ int msa_dense_attn_varlen_backward(const msa_params *p, int nq, int nk, const ms
   a.out = const_cast<msa_bf16 *>(out);
   a.lse = const_cast<float *>(lse);
   a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv;
-  cudaError_t e =
-      msa::launch_dense_varlen_backward(a, num_sms(), reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap tq, tdo, tk, tv;
+  rc = make_packed_q_tmap(&tq, nq > 0 ? q : k, p, nq > 0 ? nq : 1);
+  if (!rc) rc = make_packed_q_tmap(&tdo, nq > 0 ? dout : k, p, nq > 0 ? nq : 1);
+  if (!rc) rc = make_packed_kv_tmap(&tk, k, p, nk, q);
+  if (!rc) rc = make_packed_kv_tmap(&tv, v, p, nk, q);
+  if (rc) return rc;
+  cudaError_t e = msa::launch_dense_varlen_backward(tq, tdo, tk, tv, a, num_sms(),
+                                                    reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dense attention backward launch");
   return MSA_OK;
 }
