@@ -33,8 +33,21 @@ namespace {
 
 constexpr int kBThreads = 384;
 constexpr int kBTile = 32768;                       // 128 rows x 256 B
-// Six tiles: two that stay for an item, two stages of two that stream.
-constexpr int kBSKeep = 0, kBSRing = 2 * kBTile, kBCtl = 6 * kBTile;
+// Seven tiles: two that stay for an item, a ring of three for the streamed
+// tile that two products far apart read (dkv: Q, dq: K) and one of two for the
+// other (dkv: dO, dq: V).  They fill the dynamic shared memory; barriers and
+// statistics lie in 3 KB of static memory before it, so that the tiles start
+// on a 1024-byte boundary without slack.
+constexpr int kBSKeep = 0, kBSLong = 2 * kBTile, kBSShort = 5 * kBTile, kBSmem = 7 * kBTile;
+constexpr int kBCtl = 3072;
+static_assert(kBSmem + kBCtl <= 232448, "shared memory budget");
+// A place in a ring of n stages and the phase of its use.
+struct RingPos {
+  uint32_t s = 0, ph = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++s == n) { s = 0; ph ^= 1; }
+  }
+};
 constexpr int kBRegsRest = 72, kBRegsSoftmax = 216;   // 128 * 72 + 256 * 216 = 384 * 168
 constexpr uint32_t kBDescHi = sdesc_hi(1024);
 
@@ -152,13 +165,12 @@ __device__ __forceinline__ bool kv_item(const DenseArgs &a, int r, int n_work, K
 }
 
 // barriers
-constexpr int kVKvFull = 0, kVKvEmpty = 1, kVQFull = 2, kVQEmpty = 4, kVStFull = 6, kVStEmpty = 8,
-              kVSFull = 10, kVDpFull = 11, kVPFull = 12, kVZFull = 13, kVAccFull = 14, kVAccEmpty = 15,
-              kVDrain = 16, kVNumBars = 17;
+constexpr int kVKvFull = 0, kVKvEmpty = 1, kVQFull = 2, kVQEmpty = 5, kVOFull = 8, kVOEmpty = 10,
+              kVStFull = 12, kVStEmpty = 14, kVSFull = 16, kVDpFull = 17, kVPFull = 18, kVZFull = 19,
+              kVAccFull = 20, kVAccEmpty = 21, kVDrain = 22, kVNumBars = 23;
 constexpr int kVMisc = kVNumBars * 8;                // tmem holder, abort flag
 constexpr int kVStat = (kVMisc + 8 + 15) & ~15;      // [2 stages][128] -lse log2 e, [2][128] -D
-constexpr int kVSmem = kBCtl + kVStat + 4 * 128 * 4 + 1024;
-static_assert(kVSmem <= 232448, "shared memory budget");
+static_assert(kVStat + 4 * 128 * 4 <= kBCtl, "control block");
 constexpr uint32_t kVTmS = 0, kVTmDP = 128, kVTmDV = 256, kVTmDK = 384;
 
 // The softmax and the UMMAs take turns on the two halves of TMEM's working
@@ -170,10 +182,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const DenseArgs a) {
   constexpr int QPI = 128 / R;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(1024) uint8_t ctl[kBCtl];
   const uint32_t s_base = smem_u32(smem);
-  uint8_t *ctl = smem + kBCtl;
+  if (s_base & 1023) {   // the tiles' swizzle needs it
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, kStatusTimeout);
+    return;
+  }
   const uint32_t bar0 = smem_u32(ctl);
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ctl + kVMisc);
@@ -208,7 +223,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
       tma_prefetch_desc(&tm_do);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      uint32_t it = 0, seq = 0;
+      uint32_t it = 0, seq = 0, nq = 0;              // items; tiles of dO and of Q
+      RingPos q, o;
       bool ok = true;
       for (int r = 0; ok && kv_item<R>(a, r, n_work, w); ++r) {
         if (w.n_qt == 0) continue;
@@ -218,57 +234,74 @@ __global__ void __launch_bounds__(kBThreads, 1)
         load_tile(s_base + kBSKeep, &tm_k, bar(kVKvFull), w.g, w.key0);
         load_tile(s_base + kBSKeep + kBTile, &tm_v, bar(kVKvFull), w.g, w.key0);
         ++it;
-        for (int i = 0; i < w.n_qt && ok; ++i) {
-          const int st = seq & 1;
-          ok = mbar_wait(bar(kVQEmpty + st), ((seq >> 1) & 1) ^ 1, abort_flag, a.status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(bar(kVQFull + st), 2 * kBTile);
+        for (int i = 0; i < w.n_qt && ok; ++i, ++seq) {
           const int row = w.q0 + (w.qt0 + i) * QPI;
-          load_tile(s_base + kBSRing + st * 2 * kBTile, &tm_q, bar(kVQFull + st), w.g * R, row);
-          load_tile(s_base + kBSRing + st * 2 * kBTile + kBTile, &tm_do, bar(kVQFull + st), w.g * R, row);
-          ++seq;
+          ok = mbar_wait(bar(kVQEmpty + q.s), q.ph ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(kVQFull + q.s), kBTile);
+          load_tile(s_base + kBSLong + q.s * kBTile, &tm_q, bar(kVQFull + q.s), w.g * R, row);
+          q.next(3);
+          ++nq;
+          ok = mbar_wait(bar(kVOEmpty + o.s), o.ph ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(kVOFull + o.s), kBTile);
+          load_tile(s_base + kBSShort + o.s * kBTile, &tm_do, bar(kVOFull + o.s), w.g * R, row);
+          o.next(2);
         }
       }
       // copies still in flight land before the CTA may exit
       if (it) mbar_wait_drain(bar(kVKvFull), (it - 1) & 1);
+      for (uint32_t x = 1; x <= 3; ++x)
+        if (nq >= x) mbar_wait_drain(bar(kVQFull + (nq - x) % 3), ((nq - x) / 3) & 1);
       for (uint32_t x = 1; x <= 2; ++x)
-        if (seq >= x) mbar_wait_drain(bar(kVQFull + ((seq - x) & 1)), ((seq - x) >> 1) & 1);
+        if (seq >= x) mbar_wait_drain(bar(kVOFull + ((seq - x) & 1)), ((seq - x) >> 1) & 1);
     } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------- MMA issuer
       const uint32_t k_lo = sdesc_lo(s_base + kBSKeep, 16), v_lo = sdesc_lo(s_base + kBSKeep + kBTile, 16);
-      const uint32_t qk_lo = sdesc_lo(s_base + kBSRing, 16), qm_lo = sdesc_lo(s_base + kBSRing, 16384);
+      // Q and dO as K-major operands and, summed over their rows, as MN-major ones
+      const uint32_t qk_lo = sdesc_lo(s_base + kBSLong, 16), qm_lo = sdesc_lo(s_base + kBSLong, 16384);
+      const uint32_t ok_lo = sdesc_lo(s_base + kBSShort, 16), om_lo = sdesc_lo(s_base + kBSShort, 16384);
       constexpr uint32_t T = kBTile >> 4;
-      uint32_t it = 0, seq = 0;
+      uint32_t it = 0, ph = 0;
+      RingPos q, o;
       bool ok = true;
       for (int r = 0; ok && kv_item<R>(a, r, n_work, w); ++r) {
         if (w.n_qt == 0) continue;
         ok = mbar_wait(bar(kVKvFull), it & 1, abort_flag, a.status) &&
-             mbar_wait(bar(kVQFull + (seq & 1)), (seq >> 1) & 1, abort_flag, a.status);
+             mbar_wait(bar(kVQFull + q.s), q.ph, abort_flag, a.status);
         if (!ok) break;
-        mma_tiles(tm + kVTmS, k_lo, qk_lo + (seq & 1) * 2 * T);
+        mma_tiles(tm + kVTmS, k_lo, qk_lo + q.s * T);
         umma_commit(bar(kVSFull));
-        mma_tiles(tm + kVTmDP, v_lo, qk_lo + (seq & 1) * 2 * T + T);
+        ok = mbar_wait(bar(kVOFull + o.s), o.ph, abort_flag, a.status);
+        if (!ok) break;
+        mma_tiles(tm + kVTmDP, v_lo, ok_lo + o.s * T);
         umma_commit(bar(kVDpFull));
         ok = mbar_wait(bar(kVAccEmpty), (it & 1) ^ 1, abort_flag, a.status);
-        for (int i = 0; i < w.n_qt && ok; ++i, ++seq) {
-          const uint32_t st = seq & 1, nx = (seq + 1) & 1;
+        for (int i = 0; i < w.n_qt && ok; ++i, ph ^= 1) {
           const bool more = i + 1 < w.n_qt;
-          if (more) ok = mbar_wait(bar(kVQFull + nx), ((seq + 1) >> 1) & 1, abort_flag, a.status);
-          ok = ok && mbar_wait(bar(kVPFull), seq & 1, abort_flag, a.status);
+          const uint32_t qs = q.s, os = o.s;
+          q.next(3);
+          o.next(2);
+          ok = mbar_wait(bar(kVPFull), ph, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          mma_from_tmem(tm + kVTmDV, tm + kVTmS, qm_lo + st * 2 * T + T, i > 0);
+          mma_from_tmem(tm + kVTmDV, tm + kVTmS, om_lo + os * T, i > 0);
+          umma_commit(bar(kVOEmpty + os));
           if (more) {
-            mma_tiles(tm + kVTmS, k_lo, qk_lo + nx * 2 * T);
+            ok = mbar_wait(bar(kVQFull + q.s), q.ph, abort_flag, a.status);
+            if (!ok) break;
+            mma_tiles(tm + kVTmS, k_lo, qk_lo + q.s * T);
             umma_commit(bar(kVSFull));
           }
-          ok = mbar_wait(bar(kVZFull), seq & 1, abort_flag, a.status);
+          ok = mbar_wait(bar(kVZFull), ph, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          mma_from_tmem(tm + kVTmDK, tm + kVTmDP, qm_lo + st * 2 * T, i > 0);
-          umma_commit(bar(kVQEmpty + st));
+          mma_from_tmem(tm + kVTmDK, tm + kVTmDP, qm_lo + qs * T, i > 0);
+          umma_commit(bar(kVQEmpty + qs));
           if (more) {
-            mma_tiles(tm + kVTmDP, v_lo, qk_lo + nx * 2 * T + T);
+            ok = mbar_wait(bar(kVOFull + o.s), o.ph, abort_flag, a.status);
+            if (!ok) break;
+            mma_tiles(tm + kVTmDP, v_lo, ok_lo + o.s * T);
             umma_commit(bar(kVDpFull));
           }
         }
@@ -300,11 +333,11 @@ __global__ void __launch_bounds__(kBThreads, 1)
             s_nd[st * 128 + x] = v.y;
           }
           if (w.n - qa < QPI) {
-            ok = mbar_wait(bar(kVQFull + st), (seq >> 1) & 1, abort_flag, a.status);
+            ok = mbar_wait(bar(kVQFull + seq % 3), (seq / 3) & 1, abort_flag, a.status) &&
+                 mbar_wait(bar(kVOFull + st), (seq >> 1) & 1, abort_flag, a.status);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            uint8_t *tile = smem + kBSRing + st * 2 * kBTile;
-            clear_rows(tile, (w.n - qa) * R, ht, 64);
-            clear_rows(tile + kBTile, (w.n - qa) * R, ht, 64);
+            clear_rows(smem + kBSLong + (seq % 3) * kBTile, (w.n - qa) * R, ht, 64);
+            clear_rows(smem + kBSShort + st * kBTile, (w.n - qa) * R, ht, 64);
             fence_proxy_async_smem();
           }
           mbar_arrive(bar(kVStFull + st));
@@ -429,11 +462,10 @@ __device__ __forceinline__ bool q_item(const DenseArgs &a, int r, int n_work, QI
   return true;
 }
 
-constexpr int kGQFull = 0, kGQEmpty = 1, kGKvFull = 2, kGKvEmpty = 4, kGSFull = 6, kGDpFull = 8, kGZFull = 9,
-              kGAccFull = 10, kGAccEmpty = 11, kGReq = 12, kGClean = 13, kGDrain = 14, kGNumBars = 15;
+constexpr int kGQFull = 0, kGQEmpty = 1, kGKFull = 2, kGKEmpty = 5, kGVFull = 8, kGVEmpty = 10, kGSFull = 12,
+              kGDpFull = 14, kGZFull = 15, kGAccFull = 16, kGAccEmpty = 17, kGReq = 18, kGClean = 19, kGDrain = 20,
+              kGNumBars = 21;
 constexpr int kGMisc = kGNumBars * 8;
-constexpr int kGSmem = kBCtl + kGMisc + 16 + 1024;
-static_assert(kGSmem <= 232448, "shared memory budget");
 constexpr uint32_t kGTmS = 0, kGTmDP = 256, kGTmDQ = 384;   // S: two buffers of 128 columns
 
 // S of key tile j+1 runs under the softmax of tile j; dP of tile j+1 and
@@ -443,10 +475,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
     dense_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const DenseArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(1024) uint8_t ctl[kBCtl];
   const uint32_t s_base = smem_u32(smem);
-  uint8_t *ctl = smem + kBCtl;
+  if (s_base & 1023) {   // the tiles' swizzle needs it
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, kStatusTimeout);
+    return;
+  }
   const uint32_t bar0 = smem_u32(ctl);
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ctl + kGMisc);
@@ -476,7 +511,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
       tma_prefetch_desc(&tm_do);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      uint32_t it = 0, seq = 0;
+      uint32_t it = 0, seq = 0, nk = 0;              // items; tiles of V and of K
+      RingPos k, v;
       bool ok = true;
       for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
         if (w.n_kt == 0) continue;
@@ -486,44 +522,58 @@ __global__ void __launch_bounds__(kBThreads, 1)
         load_tile(s_base + kBSKeep, &tm_q, bar(kGQFull), w.g * R, w.q0);
         load_tile(s_base + kBSKeep + kBTile, &tm_do, bar(kGQFull), w.g * R, w.q0);
         ++it;
-        for (int j = 0; j < w.n_kt && ok; ++j) {
-          const int st = seq & 1;
-          ok = mbar_wait(bar(kGKvEmpty + st), ((seq >> 1) & 1) ^ 1, abort_flag, a.status);
+        for (int j = 0; j < w.n_kt && ok; ++j, ++seq) {
+          ok = mbar_wait(bar(kGKEmpty + k.s), k.ph ^ 1, abort_flag, a.status);
           if (!ok) break;
-          mbar_arrive_expect_tx(bar(kGKvFull + st), 2 * kBTile);
-          load_tile(s_base + kBSRing + st * 2 * kBTile, &tm_k, bar(kGKvFull + st), w.g, w.key0 + j * 128);
-          load_tile(s_base + kBSRing + st * 2 * kBTile + kBTile, &tm_v, bar(kGKvFull + st), w.g, w.key0 + j * 128);
-          ++seq;
+          mbar_arrive_expect_tx(bar(kGKFull + k.s), kBTile);
+          load_tile(s_base + kBSLong + k.s * kBTile, &tm_k, bar(kGKFull + k.s), w.g, w.key0 + j * 128);
+          k.next(3);
+          ++nk;
+          ok = mbar_wait(bar(kGVEmpty + v.s), v.ph ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(kGVFull + v.s), kBTile);
+          load_tile(s_base + kBSShort + v.s * kBTile, &tm_v, bar(kGVFull + v.s), w.g, w.key0 + j * 128);
+          v.next(2);
         }
       }
       if (it) mbar_wait_drain(bar(kGQFull), (it - 1) & 1);
+      for (uint32_t x = 1; x <= 3; ++x)
+        if (nk >= x) mbar_wait_drain(bar(kGKFull + (nk - x) % 3), ((nk - x) / 3) & 1);
       for (uint32_t x = 1; x <= 2; ++x)
-        if (seq >= x) mbar_wait_drain(bar(kGKvFull + ((seq - x) & 1)), ((seq - x) >> 1) & 1);
+        if (seq >= x) mbar_wait_drain(bar(kGVFull + ((seq - x) & 1)), ((seq - x) >> 1) & 1);
     } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------- MMA issuer
       const uint32_t q_lo = sdesc_lo(s_base + kBSKeep, 16), do_lo = sdesc_lo(s_base + kBSKeep + kBTile, 16);
-      const uint32_t kk_lo = sdesc_lo(s_base + kBSRing, 16), km_lo = sdesc_lo(s_base + kBSRing, 16384);
+      const uint32_t kk_lo = sdesc_lo(s_base + kBSLong, 16), km_lo = sdesc_lo(s_base + kBSLong, 16384);
+      const uint32_t vk_lo = sdesc_lo(s_base + kBSShort, 16);
       constexpr uint32_t T = kBTile >> 4;
       uint32_t it = 0, seq = 0, cn = 0;
+      RingPos k, v;
       bool ok = true;
       for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
         if (w.n_kt == 0) continue;
         ok = mbar_wait(bar(kGQFull), it & 1, abort_flag, a.status) &&
-             mbar_wait(bar(kGKvFull + (seq & 1)), (seq >> 1) & 1, abort_flag, a.status);
+             mbar_wait(bar(kGKFull + k.s), k.ph, abort_flag, a.status);
         if (!ok) break;
-        mma_tiles(tm + kGTmS + (seq & 1) * 128, q_lo, kk_lo + (seq & 1) * 2 * T);
+        mma_tiles(tm + kGTmS + (seq & 1) * 128, q_lo, kk_lo + k.s * T);
         umma_commit(bar(kGSFull + (seq & 1)));
-        mma_tiles(tm + kGTmDP, do_lo, kk_lo + (seq & 1) * 2 * T + T);
+        ok = mbar_wait(bar(kGVFull + v.s), v.ph, abort_flag, a.status);
+        if (!ok) break;
+        mma_tiles(tm + kGTmDP, do_lo, vk_lo + v.s * T);
         umma_commit(bar(kGDpFull));
+        umma_commit(bar(kGVEmpty + v.s));
+        v.next(2);
         ok = mbar_wait(bar(kGAccEmpty), (it & 1) ^ 1, abort_flag, a.status);
         for (int j = 0; j < w.n_kt && ok; ++j, ++seq) {
-          const uint32_t st = seq & 1, nx = (seq + 1) & 1;
+          const uint32_t st = seq & 1, ks = k.s;
           const bool more = j + 1 < w.n_kt;
+          k.next(3);
           if (more) {
-            ok = mbar_wait(bar(kGKvFull + nx), ((seq + 1) >> 1) & 1, abort_flag, a.status);
+            ok = mbar_wait(bar(kGKFull + k.s), k.ph, abort_flag, a.status);
             if (!ok) break;
-            mma_tiles(tm + kGTmS + nx * 128, q_lo, kk_lo + nx * 2 * T);
-            umma_commit(bar(kGSFull + nx));
+            mma_tiles(tm + kGTmS + (st ^ 1) * 128, q_lo, kk_lo + k.s * T);
+            umma_commit(bar(kGSFull + (st ^ 1)));
+            ok = mbar_wait(bar(kGVFull + v.s), v.ph, abort_flag, a.status);
           } else if (w.m - j * 128 < 128) {   // K's rows behind the last key are cleared
             mbar_arrive(bar(kGReq));
             ok = mbar_wait(bar(kGClean), cn & 1, abort_flag, a.status);
@@ -533,11 +583,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (more) {
-            mma_tiles(tm + kGTmDP, do_lo, kk_lo + nx * 2 * T + T);
+            mma_tiles(tm + kGTmDP, do_lo, vk_lo + v.s * T);
             umma_commit(bar(kGDpFull));
+            umma_commit(bar(kGVEmpty + v.s));
+            v.next(2);
           }
-          mma_from_tmem(tm + kGTmDQ, tm + kGTmS + st * 128, km_lo + st * 2 * T, j > 0);
-          umma_commit(bar(kGKvEmpty + st));
+          mma_from_tmem(tm + kGTmDQ, tm + kGTmS + st * 128, km_lo + ks * T, j > 0);
+          umma_commit(bar(kGKEmpty + ks));
         }
         if (!ok) break;
         umma_commit(bar(kGAccFull));
@@ -559,10 +611,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
         if (w.n_kt == 0 || rem >= 128) continue;
         const uint32_t last = seq - 1;
         ok = mbar_wait(bar(kGReq), cn & 1, abort_flag, a.status) &&
-             mbar_wait(bar(kGKvFull + (last & 1)), (last >> 1) & 1, abort_flag, a.status);
+             mbar_wait(bar(kGKFull + last % 3), (last / 3) & 1, abort_flag, a.status);
         ++cn;
         if (!__all_sync(0xffffffffu, ok)) break;
-        clear_rows(smem + kBSRing + (last & 1) * 2 * kBTile, rem, lane, 32);
+        clear_rows(smem + kBSLong + (last % 3) * kBTile, rem, lane, 32);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kGClean));
@@ -647,15 +699,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
 template <int R>
 cudaError_t launch_bwd_r(const CUtensorMap &tq, const CUtensorMap &tdo, const CUtensorMap &tk,
                          const CUtensorMap &tv, const DenseArgs &a, int num_sms, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(dense_dkv_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kVSmem);
+  cudaError_t e = cudaFuncSetAttribute(dense_dkv_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBSmem);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(dense_dq_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
+  e = cudaFuncSetAttribute(dense_dq_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBSmem);
   if (e != cudaSuccess) return e;
   const long long wk = (long long)a.max_items_k * a.G, wq = (long long)a.max_items * a.G;
   if (a.nk > 0)
-    dense_dkv_kernel<R><<<unsigned(wk < num_sms ? wk : num_sms), kBThreads, kVSmem, st>>>(tq, tdo, tk, tv, a);
+    dense_dkv_kernel<R><<<unsigned(wk < num_sms ? wk : num_sms), kBThreads, kBSmem, st>>>(tq, tdo, tk, tv, a);
   if (a.nq > 0)
-    dense_dq_kernel<R><<<unsigned(wq < num_sms ? wq : num_sms), kBThreads, kGSmem, st>>>(tq, tdo, tk, tv, a);
+    dense_dq_kernel<R><<<unsigned(wq < num_sms ? wq : num_sms), kBThreads, kBSmem, st>>>(tq, tdo, tk, tv, a);
   return cudaGetLastError();
 }
 
