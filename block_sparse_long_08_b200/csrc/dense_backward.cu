@@ -8,7 +8,7 @@
 //                 that sees one of them.  Transposed products, so that what
 //                 the softmax makes is the A operand from TMEM:
 //                   S^T = K Q^T, dP^T = V dO^T   (TMEM lanes are keys)
-//                   dV += P^T dO, dK += dZ^T Q   (P^T, dZ^T over S^T, dP^T)
+//                   dV += P^T dO, dK += dZ^T Q   (P^T and dZ^T over dP^T)
 //   dense_dq_kernel    query tiles outer: one item is a 128-row query tile:
 //                   S = Q K^T, dP = dO V^T, dQ += dZ K  (dZ over S).
 //
@@ -70,7 +70,8 @@ __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a_lo, uint32_t b_
   }
 }
 // D (+)= A B: A from TMEM (bf16 pairs, the first 64 of the 128 summed-over
-// indices at `a`, the others at a + 64), B a tile whose rows are summed over.
+// indices from column `a`, the others from a + 64), B a tile whose rows are
+// summed over.
 __device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint32_t b_lo, bool add) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 1);
 #pragma unroll
@@ -167,15 +168,18 @@ __device__ __forceinline__ bool kv_item(const DenseArgs &a, int r, int n_work, K
 // barriers
 constexpr int kVKvFull = 0, kVKvEmpty = 1, kVQFull = 2, kVQEmpty = 5, kVOFull = 8, kVOEmpty = 10,
               kVStFull = 12, kVStEmpty = 14, kVSFull = 16, kVDpFull = 17, kVPFull = 18, kVZFull = 19,
-              kVAccFull = 20, kVAccEmpty = 21, kVDrain = 22, kVNumBars = 23;
+              kVAccFull = 20, kVAccEmpty = 21, kVDrain = 22, kVSFree = 23, kVNumBars = 24;
 constexpr int kVMisc = kVNumBars * 8;                // tmem holder, abort flag
 constexpr int kVStat = (kVMisc + 8 + 15) & ~15;      // [2 stages][128] -lse log2 e, [2][128] -D
 static_assert(kVStat + 4 * 128 * 4 <= kBCtl, "control block");
 constexpr uint32_t kVTmS = 0, kVTmDP = 128, kVTmDV = 256, kVTmDK = 384;
 
-// The softmax and the UMMAs take turns on the two halves of TMEM's working
-// columns: while the softmax makes P of tile i, dK += dZ Q of tile i-1 and dP
-// of tile i run; while it makes dZ of tile i, dV += P dO and S of tile i+1.
+// S is free as soon as the softmax has it in registers, and P and dZ both go
+// over dP (each warpgroup's 64 columns of it take its 32 of P and its 32 of
+// dZ once it has read them), so the order of the UMMAs is
+//   dV += P_i dO_i | dK += dZ_i Q_i, dP_i+1, S_i+2
+// (the bar: behind P_i, behind dZ_i) and the exponentials of tile i+1 run
+// under all of it: about 2000 cycles of softmax over 2240 of products.
 template <int R>
 __global__ void __launch_bounds__(kBThreads, 1)
     dense_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -198,7 +202,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kVNumBars; ++i)
       mbar_init(bar(i), i == kVStFull || i == kVStFull + 1 ? 64
-                        : (i == kVStEmpty || i == kVStEmpty + 1 || i == kVPFull || i == kVZFull || i == kVAccEmpty)
+                        : (i == kVStEmpty || i == kVStEmpty + 1 || i == kVPFull || i == kVZFull || i == kVAccEmpty ||
+                         i == kVSFree)
                             ? 256
                             : 1);
     *abort_flag = 0;
@@ -270,39 +275,53 @@ __global__ void __launch_bounds__(kBThreads, 1)
         ok = mbar_wait(bar(kVKvFull), it & 1, abort_flag, a.status) &&
              mbar_wait(bar(kVQFull + q.s), q.ph, abort_flag, a.status);
         if (!ok) break;
-        mma_tiles(tm + kVTmS, k_lo, qk_lo + q.s * T);
-        umma_commit(bar(kVSFull));
+        // S of the first two tiles, dP of the first; qn runs ahead with S
+        RingPos qn = q;
+        auto issue_s = [&]() {
+          mma_tiles(tm + kVTmS, k_lo, qk_lo + qn.s * T);
+          umma_commit(bar(kVSFull));
+          qn.next(3);
+        };
+        issue_s();
         ok = mbar_wait(bar(kVOFull + o.s), o.ph, abort_flag, a.status);
         if (!ok) break;
         mma_tiles(tm + kVTmDP, v_lo, ok_lo + o.s * T);
         umma_commit(bar(kVDpFull));
+        if (w.n_qt > 1) {
+          ok = mbar_wait(bar(kVQFull + qn.s), qn.ph, abort_flag, a.status) &&
+               mbar_wait(bar(kVSFree), ph, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s();
+        }
         ok = mbar_wait(bar(kVAccEmpty), (it & 1) ^ 1, abort_flag, a.status);
         for (int i = 0; i < w.n_qt && ok; ++i, ph ^= 1) {
-          const bool more = i + 1 < w.n_qt;
           const uint32_t qs = q.s, os = o.s;
           q.next(3);
           o.next(2);
           ok = mbar_wait(bar(kVPFull), ph, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          mma_from_tmem(tm + kVTmDV, tm + kVTmS, om_lo + os * T, i > 0);
+          mma_from_tmem(tm + kVTmDV, tm + kVTmDP, om_lo + os * T, i > 0);
           umma_commit(bar(kVOEmpty + os));
-          if (more) {
-            ok = mbar_wait(bar(kVQFull + q.s), q.ph, abort_flag, a.status);
-            if (!ok) break;
-            mma_tiles(tm + kVTmS, k_lo, qk_lo + q.s * T);
-            umma_commit(bar(kVSFull));
-          }
-          ok = mbar_wait(bar(kVZFull), ph, abort_flag, a.status);
+          if (i + 1 < w.n_qt) ok = mbar_wait(bar(kVOFull + o.s), o.ph, abort_flag, a.status);
+          ok = ok && mbar_wait(bar(kVZFull), ph, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          mma_from_tmem(tm + kVTmDK, tm + kVTmDP, qm_lo + qs * T, i > 0);
+          mma_from_tmem(tm + kVTmDK, tm + kVTmDP + 32, qm_lo + qs * T, i > 0);
           umma_commit(bar(kVQEmpty + qs));
-          if (more) {
-            ok = mbar_wait(bar(kVOFull + o.s), o.ph, abort_flag, a.status);
-            if (!ok) break;
+          if (i + 1 < w.n_qt) {
             mma_tiles(tm + kVTmDP, v_lo, ok_lo + o.s * T);
             umma_commit(bar(kVDpFull));
+          }
+          // the softmax's read of S_i+1 (of the last tile too, so that every
+          // phase of the barrier is waited for)
+          if (i + 2 < w.n_qt) ok = mbar_wait(bar(kVQFull + qn.s), qn.ph, abort_flag, a.status);
+          if (i + 1 < w.n_qt) ok = ok && mbar_wait(bar(kVSFree), ph ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          if (i + 2 < w.n_qt) {
+            tc_fence_after();
+            issue_s();
           }
         }
         if (!ok) break;
@@ -372,6 +391,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
         tc_fence_after();
         float p[64];
         load64(tl + kVTmS + hc * 64, p);
+        tc_fence_before();
+        mbar_arrive(bar(kVSFree));
         // rows that see this key: query qa + row / R >= key - rel, up to the last query
         const int lo = (key - w.rel - qa) * R - hc * 64, hi = (w.n - qa) * R - hc * 64;
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
@@ -390,14 +411,14 @@ __global__ void __launch_bounds__(kBThreads, 1)
 #pragma unroll
           for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
         }
-        store64(tl + kVTmS + hc * 64, p);
-        tc_fence_before();
-        mbar_arrive(bar(kVPFull));
         ok = mbar_wait(bar(kVDpFull), seq & 1, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         float z[64];
         load64(tl + kVTmDP + hc * 64, z);
+        store64(tl + kVTmDP + hc * 64, p);
+        tc_fence_before();
+        mbar_arrive(bar(kVPFull));
         const float4 *nd = reinterpret_cast<const float4 *>(s_nd + st * 128 + hc * 64);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -413,7 +434,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
 #pragma unroll
           for (int c = 0; c < 64; ++c) z[c] = (c >= lo && c < hi) ? z[c] : 0.f;
         }
-        store64(tl + kVTmDP + hc * 64, z);
+        store64(tl + kVTmDP + hc * 64 + 32, z);
         tc_fence_before();
         mbar_arrive(bar(kVZFull));
         mbar_arrive(bar(kVStEmpty + st));
