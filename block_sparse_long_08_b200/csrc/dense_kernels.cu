@@ -26,7 +26,7 @@
 // products of both then finish late), S held back to interleave it with the
 // other tile's O (the tiles fall into step: 3.2 ms).
 //
-// Roles (one persistent CTA per SM, three warpgroups):
+// Roles (one persistent CTA per SM, four warpgroups):
 //   warp 0     TMA producer: the tiles' Q, then K and V of each key tile, into
 //              a ring of five 32 KB tiles.
 //   warp 1     TMEM owner; one thread issues the UMMAs.  Per key tile j:
@@ -41,6 +41,8 @@
 //              moves only when a tile raises the row's maximum by more than
 //              2^8 in P; O and the row's sum are then scaled in place, a few
 //              times per row at most.
+//   warps 12-15  epilogue of both tiles: O / l as bf16 and lse, while the
+//              softmax is at the next item.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -168,7 +170,8 @@ __global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int
 }
 
 // ------------------------------------------------------------------ forward
-constexpr int kFThreads = 384;
+constexpr int kFThreads = 512;
+constexpr int kFRegsRest = 64, kFRegsSoftmax = 192;   // 256 threads each: 512 * 128 in all
 constexpr int kFTile = 32768;                    // 128 rows x 256 B
 constexpr int kFNkv = 5;                         // K/V ring depth
 constexpr int kFSQ = 0;                          // two Q tiles
@@ -177,11 +180,14 @@ constexpr int kFCtl = kFSKV + kFNkv * kFTile;
 // barriers
 constexpr int kFQFull = 0, kFQEmpty = 2, kFKvFull = 4, kFKvEmpty = 4 + kFNkv,
               kFSFull = 4 + 2 * kFNkv, kFPFull = kFSFull + 2, kFOFull = kFPFull + 2,
-              kFOEmpty = kFOFull + 2, kFDrain = kFOEmpty + 2, kFVReq = kFDrain + 1, kFVClean = kFVReq + 1,
+              kFOEmpty = kFOFull + 2, kFLFull = kFOEmpty + 2, kFDrain = kFLFull + 2, kFVReq = kFDrain + 1, kFVClean = kFVReq + 1,
               kFNumBars = kFVClean + 1;
 constexpr int kFCtlMisc = kFNumBars * 8;         // tmem holder, abort flag
-constexpr int kFSmem = kFCtl + kFCtlMisc + 16 + 1024;
-static_assert(kFSmem <= 232448, "shared memory budget");
+constexpr int kFCtlX = (kFCtlMisc + 8 + 15) & ~15;   // [2][128] row sums, [2][128] reference maxima
+constexpr int kFBytes = kFCtlX + 4 * 128 * 4;
+static_assert(kFBytes <= 3072, "control block");
+constexpr int kFSmem = kFCtl;
+static_assert(kFSmem + 3072 <= 232448, "shared memory budget");
 // TMEM columns: S (then P) of tile A and B, O of A and B
 constexpr uint32_t kFTmS = 0, kFTmO = 256;
 
@@ -235,11 +241,16 @@ __global__ void __launch_bounds__(kFThreads, 1)
     dense_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const DenseArgs a) {
   constexpr int QPI = 128 / R;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~uintptr_t(1023));
+  // the tiles fill the dynamic memory; 3 KB of static memory before them, so
+  // that they start on a 1024-byte boundary without slack
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(1024) uint8_t ctl[3072];
   const uint32_t s_base = smem_u32(smem);
-  uint8_t *ctl = smem + kFCtl;
+  if (s_base & 1023) {   // the tiles' swizzle needs it
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, kStatusTimeout);
+    return;
+  }
+  float *s_l = reinterpret_cast<float *>(ctl + kFCtlX), *s_m = s_l + 256;
   const uint32_t bar0 = smem_u32(ctl);
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ctl + kFCtlMisc);
@@ -256,6 +267,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       mbar_init(bar(kFPFull + x), 128);
       mbar_init(bar(kFOFull + x), 1);
       mbar_init(bar(kFOEmpty + x), 128);
+      mbar_init(bar(kFLFull + x), 128);
     }
     for (int x = 0; x < kFNkv; ++x) {
       mbar_init(bar(kFKvFull + x), 1);
@@ -279,7 +291,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const int n_work = *a.n_items * a.G;
 
   if (warp < 4) {
-    regs_dec<72>();
+    regs_dec<kFRegsRest>();
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------- TMA producer
       tma_prefetch_desc(&tm_q);
@@ -435,32 +447,23 @@ __global__ void __launch_bounds__(kFThreads, 1)
         if (lane == 0) mbar_arrive(bar(kFVClean));
       }
     }
-  } else {
+  } else if (warp < 12) {
     // ---------------------------------------------------------- softmax
-    regs_inc<216>();
+    regs_inc<kFRegsSoftmax>();
     const int x = (warp - 4) >> 2;              // tile A or B
     const int row = (warp & 3) * 32 + lane;     // tile row = TMEM lane
     const uint32_t tm_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t tm_s = tm_lane + kFTmS + x * 128, tm_o = tm_lane + kFTmO + x * 128;
-    const int qi = row / R, hh = row % R;
+    const int qi = row / R;
     const float2 sc2 = f2_dup(a.scale_log2);
-    uint32_t sn = 0, on = 0;
+    uint32_t sn = 0;
     bool ok = true;
     FItem w;
     for (int r = 0; ok && dense_item<R>(a, r, n_work, w); ++r) {
       const bool valid = x * QPI + qi < w.n;
       const int n_kt = w.n_kt(x);
       const int hi = valid ? w.hi0 + x * QPI + qi : -1;     // last visible key
-      const size_t orow = size_t(w.q0 + x * QPI + qi) * a.H + w.g * R + hh;
-      if (n_kt == 0) {                               // no row of the tile sees a key
-        if (valid) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-          if (a.lse) a.lse[orow] = -INFINITY;
-        }
-        continue;
-      }
+      if (n_kt == 0) continue;                       // no row of the tile sees a key
       float mr = -INFINITY;                          // reference maximum, raw scores
       float2 l2 = make_float2(0.f, 0.f), l3 = l2;
       for (int j = 0; j < n_kt; ++j) {
@@ -538,36 +541,56 @@ __global__ void __launch_bounds__(kFThreads, 1)
         mbar_arrive(bar(kFPFull + x));
       }
       if (!ok) break;
-      // ---- O / l
-      ok = mbar_wait(bar(kFOFull + x), on & 1, abort_flag, a.status);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      ++on;
-      tc_fence_after();
-      float o[128];
-      {
-        float t0[32], t1[32], t2[32], t3[32];
-        tmem_ld32(tm_o, t0);
-        tmem_ld32(tm_o + 32, t1);
-        tmem_ld32(tm_o + 64, t2);
-        tmem_ld32(tm_o + 96, t3);
-        tmem_wait_ld();
+      // the sum and the maximum go to the epilogue (which has read the last
+      // item's before it freed O, without which this item has no end)
+      s_l[x * 128 + row] = (l2.x + l3.x) + (l2.y + l3.y);
+      s_m[x * 128 + row] = mr;
+      mbar_arrive(bar(kFLFull + x));
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    regs_dec<kFRegsRest>();
+    const int row = (warp & 3) * 32 + lane;          // tile row = TMEM lane
+    const uint32_t tm_lane = tmem_base + (uint32_t((warp & 3) * 32) << 16);
+    const int qi = row / R, hh = row % R;
+    uint32_t on0 = 0, on1 = 0;
+    bool ok = true;
+    FItem w;
+    for (int r = 0; ok && dense_item<R>(a, r, n_work, w); ++r) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          o[c] = t0[c];
-          o[32 + c] = t1[c];
-          o[64 + c] = t2[c];
-          o[96 + c] = t3[c];
-        }
-      }
-      tc_fence_before();
-      mbar_arrive(bar(kFOEmpty + x));
-      if (valid) {
-        const float l = (l2.x + l3.x) + (l2.y + l3.y);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+      for (int x = 0; x < 2; ++x) {
+        const bool valid = x * QPI + qi < w.n;
+        const size_t orow = size_t(w.q0 + x * QPI + qi) * a.H + w.g * R + hh;
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim);
+        if (w.n_kt(x) == 0) {                        // no row of the tile sees a key
+          if (valid) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) dst[c] = pack8_scaled(o + 8 * c, inv);
-        if (a.lse) a.lse[orow] = l > 0.f ? mr * a.scale + logf(l) : -INFINITY;
+            for (int c = 0; c < 16; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse) a.lse[orow] = -INFINITY;
+          }
+          continue;
+        }
+        uint32_t &on = x ? on1 : on0;
+        ok = ok && mbar_wait(bar(kFLFull + x), on, abort_flag, a.status) &&
+             mbar_wait(bar(kFOFull + x), on, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        on ^= 1;
+        const float l = s_l[x * 128 + row], mr = s_m[x * 128 + row];
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(tm_lane + kFTmO + x * 128 + c * 32, o);
+          tmem_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[4 * c + e] = pack8_scaled(o + 8 * e, inv);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar(kFOEmpty + x));
+        if (valid && a.lse) a.lse[orow] = l > 0.f ? mr * a.scale + logf(l) : -INFINITY;
       }
     }
   }

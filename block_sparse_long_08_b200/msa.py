@@ -727,32 +727,64 @@ def msa_sparse_attn_decode_noalloc(q, q_idx, k_cache, v_cache, k_idx_cache, seq_
 
 
 # ---- dense attention over paged caches and packed sequences (see include/msa.h)
+#
+# Single-token calls take a few microseconds on the device, so these functions
+# check each tensor in one expression and name what is wrong only when it
+# fails, pass addresses as plain integers, and leave the size of a given
+# workspace to the library's own check.
 
-def _one_device(dev, *named):
-    """Every tensor of a call lies on one device."""
-    for n, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, the call's tensors are on {dev}")
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _fits(t, name: str, dtype, numel: int, dev) -> int:
+    """Address of a tensor of the call: of this type, on the call's device,
+    contiguous, with at least the elements the call reads or writes."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev
+            or not t.is_contiguous() or t.numel() < numel):
+        if isinstance(t, torch.Tensor) and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+        _size(t, name, dtype, numel)
+        raise ValueError(f"{name} does not fit the call")
+    return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev):
+    """The call's stream handle: torch's current stream on the call's device
+    unless one is given (its raw handle where torch offers it: building the
+    Stream object takes 3 us, the whole single-token append 5)."""
+    if stream is None and _raw_stream is not None and dev.type == "cuda":
+        return _raw_stream(dev.index)
+    return _stream(stream)
 
 
 class _on_device:
-    """The call's device as the current one: streams, launches and the SM
-    count the library asks for belong to the device of the tensors."""
+    """The call's device as the current one (streams, launches and the SM
+    count the library asks for belong to the device of the tensors)."""
+
+    __slots__ = ("want", "back")
 
     def __init__(self, dev):
         self.want = dev.index if dev.type == "cuda" else None
 
     def __enter__(self):
         self.back = None
-        if self.want is not None:
-            cur = torch.cuda.current_device()
-            if cur != self.want:
-                self.back = cur
-                torch.cuda.set_device(self.want)
+        if self.want is not None and torch.cuda.current_device() != self.want:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.want)
 
     def __exit__(self, *exc):
         if self.back is not None:
             torch.cuda.set_device(self.back)
+
+
+def _call_ws(ws, p, op, dev):
+    """(workspace, its address and size): allocated for the call when None."""
+    if ws is None:
+        ws = torch.zeros(msa_workspace_bytes(p, op), dtype=_U8, device=dev)
+    return ws, _fits(ws, "ws", _U8, 0, dev), ws.numel()
 
 
 def new_paged_workspace(op: int, page_table, page_size: int, H: int, G: int) -> torch.Tensor:
@@ -768,27 +800,27 @@ def new_dense_workspace(op: int, q, k, B: int) -> torch.Tensor:
                          q.device)
 
 
-def _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G):
-    """The cache's checks: k_pages, v_pages [num_pages, page_size, G, d]."""
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or page_table.dim() != 2:
+def _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G, d, dev):
+    """The cache's checks: k_pages, v_pages [num_pages, page_size, G, d] ->
+    the C struct, page_table's rows and the tokens a row can hold."""
+    shape, cols = k_pages.shape, page_table.shape
+    if len(shape) != 4 or v_pages.shape != shape or len(cols) != 2:
         raise ValueError("k_pages, v_pages must be [num_pages, page_size, G, d], page_table [B, cols]")
     if (k_scale is None) != (v_scale is None):
         raise ValueError("an 8-bit cache needs both k_scale and v_scale")
-    num, page, g, d = k_pages.shape
+    num, page, g, dc = shape
     if g != G:
         raise ValueError(f"the cache has {g} KV heads, the call {G}")
-    kind = torch.bfloat16 if k_scale is None else torch.uint8
-    _req(k_pages, "k_pages", kind)
-    _req(v_pages, "v_pages", kind)
-    _req(page_table, "page_table", torch.int32)
+    if dc != d:
+        raise ValueError(f"the cache's head dim is {dc}, the call's {d}")
+    ks = vs = None
     if k_scale is not None:
-        _size(k_scale, "k_scale", torch.float32, num * page * G)
-        _size(v_scale, "v_scale", torch.float32, num * page * G)
-    c = msa_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(),
-                        k_scale.data_ptr() if k_scale is not None else None,
-                        v_scale.data_ptr() if v_scale is not None else None,
-                        page_table.data_ptr(), num, page, page_table.shape[1])
-    return c, page_table.shape[0], page_table.shape[1] * page, d
+        ks = _fits(k_scale, "k_scale", _F32, num * page * G, dev)
+        vs = _fits(v_scale, "v_scale", _F32, num * page * G, dev)
+    kind = _BF16 if ks is None else _U8
+    c = msa_paged_cache(_fits(k_pages, "k_pages", kind, 0, dev), _fits(v_pages, "v_pages", kind, 0, dev),
+                        ks, vs, _fits(page_table, "page_table", _I32, 0, dev), num, page, cols[1])
+    return c, cols[0], cols[1] * page
 
 
 def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=None, q=None,
@@ -801,44 +833,37 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
     (None: one row per sequence), all int32.  rot_dim defaults to twice
     inv_freq's length.  Returns q_out (allocated unless given; None without
     q); k_out, when given, receives the rotated keys."""
+    _req(k, "k", _BF16)
     N, G, d = k.shape
-    for n_, t in (("k", k), ("v", v)):
-        _size(t, n_, torch.bfloat16, N * G * d)
-    c, B, L, dc = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G)
-    if dc != d:
-        raise ValueError(f"the cache's head dim is {dc}, the keys' {d}")
-    _size(seq_lens, "seq_lens", torch.int32, B)
-    if cu_new is not None:
-        _size(cu_new, "cu_new", torch.int32, B + 1)
-    elif N != B:
+    dev = k.device
+    kv = N * G * d
+    c, B, L = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G, d, dev)
+    if cu_new is None and N != B:
         raise ValueError(f"{N} rows for {B} sequences need cu_new")
     if rot_dim is None:
         rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if rot_dim:
-        if inv_freq is None:
-            raise ValueError("rot_dim needs inv_freq")
-        _size(inv_freq, "inv_freq", torch.float32, rot_dim // 2)
+    if rot_dim and inv_freq is None:
+        raise ValueError("rot_dim needs inv_freq")
     H = G
+    qa = qo = None
     if q is not None:
         H = q.shape[1]
-        _size(q, "q", torch.bfloat16, N * H * d)
+        qa = _fits(q, "q", _BF16, N * H * d, dev)
         q_out = torch.empty_like(q) if q_out is None else q_out
-        _size(q_out, "q_out", torch.bfloat16, N * H * d)
+        qo = _fits(q_out, "q_out", _BF16, N * H * d, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if k_out is not None:
-        _size(k_out, "k_out", torch.bfloat16, N * G * d)
-    _one_device(k.device, ("v", v), ("k_pages", k_pages), ("v_pages", v_pages),
-                ("page_table", page_table), ("seq_lens", seq_lens), ("cu_new", cu_new), ("q", q),
-                ("q_out", q_out), ("k_out", k_out), ("inv_freq", inv_freq), ("k_scale", k_scale),
-                ("v_scale", v_scale), ("ws", ws))
+    va = _fits(v, "v", _BF16, kv, dev)
+    la = _fits(seq_lens, "seq_lens", _I32, B, dev)
+    cu = None if cu_new is None else _fits(cu_new, "cu_new", _I32, B + 1, dev)
+    fa = _fits(inv_freq, "inv_freq", _F32, rot_dim // 2, dev) if rot_dim else None
+    ko = None if k_out is None else _fits(k_out, "k_out", _BF16, kv, dev)
     p = make_params(B, L, H, G, d)
-    with _on_device(k.device):
-        ws = _ensure_ws(ws, p, MSA_OP_PAGED_APPEND, k.device)
-        _check(lib().msa_paged_append(ctypes.byref(p), ctypes.byref(c), N, _ptr(q), _ptr(k), _ptr(v),
-                                      _ptr(cu_new), _ptr(seq_lens), _ptr(inv_freq), int(rot_dim),
-                                      int(bool(interleaved)), _ptr(q_out), _ptr(k_out), _ptr(ws),
-                                      ws.numel(), _stream(stream)))
+    with _on_device(dev):
+        ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_APPEND, dev)
+        _check(lib().msa_paged_append(ctypes.byref(p), ctypes.byref(c), N, qa, k.data_ptr(), va, cu, la,
+                                      fa, int(rot_dim), int(bool(interleaved)), qo, ko, wa, wn,
+                                      _stream_on(stream, dev)))
     return q_out
 
 
@@ -848,43 +873,38 @@ def msa_paged_attn_decode(q, k_pages, v_pages, page_table, seq_lens, *, k_scale=
     """Dense attention of one new token per sequence, q [B,H,d], over the
     first seq_lens[b] tokens of a paged cache (see msa_paged_append) ->
     out [B,H,d] (and lse [B,H] when want_lse or given)."""
+    _req(q, "q", _BF16)
     B, H, d = q.shape
-    _req(q, "q", torch.bfloat16)
+    dev = q.device
     G = k_pages.shape[2]
-    c, Bt, L, dc = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G)
-    if dc != d or Bt < B:
-        raise ValueError(f"cache head dim {dc}, page_table rows {Bt}: the call has {d} and {B}")
-    _size(seq_lens, "seq_lens", torch.int32, B)
+    c, Bt, L = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G, d, dev)
+    if Bt < B:
+        raise ValueError(f"page_table rows: the call needs {B}, there are {Bt}")
+    la = _fits(seq_lens, "seq_lens", _I32, B, dev)
     out = torch.empty_like(q) if out is None else out
-    _size(out, "out", torch.bfloat16, B * H * d)
+    oa = _fits(out, "out", _BF16, B * H * d, dev)
     if lse is None and want_lse:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _size(lse, "lse", torch.float32, B * H)
-    _one_device(q.device, ("k_pages", k_pages), ("v_pages", v_pages), ("page_table", page_table),
-                ("seq_lens", seq_lens), ("k_scale", k_scale), ("v_scale", v_scale), ("out", out),
-                ("lse", lse), ("ws", ws))
+        lse = torch.empty((B, H), dtype=_F32, device=dev)
+    ea = None if lse is None else _fits(lse, "lse", _F32, B * H, dev)
     p = make_params(B, L, H, G, d, scale=scale)
-    with _on_device(q.device):
-        ws = _ensure_ws(ws, p, MSA_OP_PAGED_DECODE, q.device)
-        _check(lib().msa_paged_attn_decode(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(seq_lens),
-                                           _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                           _stream(stream)))
+    with _on_device(dev):
+        ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_DECODE, dev)
+        _check(lib().msa_paged_attn_decode(ctypes.byref(p), ctypes.byref(c), q.data_ptr(), la, oa, ea,
+                                           wa, wn, _stream_on(stream, dev)))
     return (out, lse) if lse is not None else out
 
 
 def _dense_inputs(q, k, v, cu_q, cu_k, scale):
+    _req(q, "q", _BF16)
     nq, H, d = q.shape
-    nk, G = k.shape[0], k.shape[1]
-    _req(q, "q", torch.bfloat16)
-    for n_, t in (("k", k), ("v", v)):
-        _size(t, n_, torch.bfloat16, nk * G * d)
-    _req(cu_q, "cu_q", torch.int32)
+    nk, G, _ = k.shape
+    dev = q.device
     B = cu_q.numel() - 1
     if B < 0:
         raise ValueError("cu_q needs one entry more than there are sequences")
-    _size(cu_k, "cu_k", torch.int32, B + 1)
-    return nq, nk, make_params(B, max(nq, nk), H, G, d, scale=scale)
+    adr = (q.data_ptr(), _fits(k, "k", _BF16, nk * G * d, dev), _fits(v, "v", _BF16, nk * G * d, dev))
+    cus = (_fits(cu_q, "cu_q", _I32, 0, dev), _fits(cu_k, "cu_k", _I32, B + 1, dev))
+    return nq, nk, make_params(B, max(nq, nk), H, G, d, scale=scale), adr, cus, dev
 
 
 def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: bool = False,
@@ -893,21 +913,17 @@ def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: 
     [nk,G,d], cu_q and cu_k [B+1] int32 (device), queries aligned to the end
     of their sequence's keys -> out [nq,H,d] (and lse [nq,H] when want_lse or
     given).  Rows behind cu_q[B] are left as they were."""
-    nq, nk, p = _dense_inputs(q, k, v, cu_q, cu_k, scale)
-    H, d = q.shape[1], q.shape[2]
+    nq, nk, p, adr, cus, dev = _dense_inputs(q, k, v, cu_q, cu_k, scale)
+    H = q.shape[1]
     out = torch.empty_like(q) if out is None else out
-    _size(out, "out", torch.bfloat16, nq * H * d)
+    oa = _fits(out, "out", _BF16, q.numel(), dev)
     if lse is None and want_lse:
-        lse = torch.empty((nq, H), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _size(lse, "lse", torch.float32, nq * H)
-    _one_device(q.device, ("k", k), ("v", v), ("cu_q", cu_q), ("cu_k", cu_k), ("out", out),
-                ("lse", lse), ("ws", ws))
-    with _on_device(q.device):
-        ws = _ensure_ws(ws, p, MSA_OP_DENSE_VARLEN, q.device)
-        _check(lib().msa_dense_attn_varlen(ctypes.byref(p), nq, nk, _ptr(q), _ptr(k), _ptr(v),
-                                           _ptr(cu_q), _ptr(cu_k), _ptr(out), _ptr(lse), _ptr(ws),
-                                           ws.numel(), _stream(stream)))
+        lse = torch.empty((nq, H), dtype=_F32, device=dev)
+    ea = None if lse is None else _fits(lse, "lse", _F32, nq * H, dev)
+    with _on_device(dev):
+        ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN, dev)
+        _check(lib().msa_dense_attn_varlen(ctypes.byref(p), nq, nk, *adr, *cus, oa, ea, wa, wn,
+                                           _stream_on(stream, dev)))
     return (out, lse) if lse is not None else out
 
 
@@ -915,24 +931,18 @@ def msa_dense_attn_varlen_backward(q, k, v, out, lse, dout, cu_q, cu_k, *, scale
                                    dq=None, dk=None, dv=None, ws=None, stream=None):
     """Gradients of msa_dense_attn_varlen: its inputs, its out [nq,H,d] and lse
     [nq,H], dout [nq,H,d] -> (dq, dk, dv) bf16, shaped like q, k, v."""
-    nq, nk, p = _dense_inputs(q, k, v, cu_q, cu_k, scale)
-    H, d, G = q.shape[1], q.shape[2], k.shape[1]
+    nq, nk, p, adr, cus, dev = _dense_inputs(q, k, v, cu_q, cu_k, scale)
+    nkv = nk * k.shape[1] * k.shape[2]
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    for n_, t in (("out", out), ("dout", dout), ("dq", dq)):
-        _size(t, n_, torch.bfloat16, nq * H * d)
-    for n_, t in (("dk", dk), ("dv", dv)):
-        _size(t, n_, torch.bfloat16, nk * G * d)
-    _size(lse, "lse", torch.float32, nq * H)
-    _one_device(q.device, ("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout),
-                ("cu_q", cu_q), ("cu_k", cu_k), ("dq", dq), ("dk", dk), ("dv", dv), ("ws", ws))
-    with _on_device(q.device):
-        ws = _ensure_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, q.device)
-        _check(lib().msa_dense_attn_varlen_backward(
-            ctypes.byref(p), nq, nk, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-            _ptr(cu_q), _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
-            _stream(stream)))
+    oa, da, qa = (_fits(t, n, _BF16, q.numel(), dev) for n, t in (("out", out), ("dout", dout), ("dq", dq)))
+    ka, va = (_fits(t, n, _BF16, nkv, dev) for n, t in (("dk", dk), ("dv", dv)))
+    ea = _fits(lse, "lse", _F32, nq * q.shape[1], dev)
+    with _on_device(dev):
+        ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, dev)
+        _check(lib().msa_dense_attn_varlen_backward(ctypes.byref(p), nq, nk, *adr, oa, ea, da, *cus, qa,
+                                                    ka, va, wa, wn, _stream_on(stream, dev)))
     return dq, dk, dv
 
 
