@@ -8,8 +8,8 @@
 namespace msa {
 
 // Checks cu_q and cu_k, writes seqs, the list of items of `per` queries and,
-// when a.items_k is given, that of key tiles (see DenseArgs).
-cudaError_t launch_dense_plan(const DenseArgs &a, int per, cudaStream_t st);
+// when a.items_k is given, that of key tiles and stat (see DenseArgs).
+cudaError_t launch_dense_plan(const DenseArgs &a, int per, int num_sms, cudaStream_t st);
 
 // Programmatic dependent launch: wait for the kernel before this one in the
 // stream, and let the next one start its own prologue.

@@ -2,7 +2,8 @@
 //   P = exp(scale q.k - lse), dP = dout . v, D = dout . out, dZ = P (dP - D)
 //   dq = scale sum dZ k,  dk += scale dZ q,  dv += P dout.
 //
-//   dense_stat_kernel  {-lse log2 e, -D} of every (query row, head).
+//   dense_plan_kernel  (dense_kernels.cu) the lists of work items, and
+//                 {-lse log2 e, -D} of every (query row, head).
 //   dense_dkv_kernel   key tiles outer: one work item is 128 keys of a KV
 //                 head and every 128-row query tile (128/R queries x R heads)
 //                 that sees one of them.  Transposed products, so that what
@@ -122,22 +123,6 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int row0, int t, int n
 __device__ __forceinline__ int round_item(int r, int n_work) {
   const int u = r * gridDim.x + ((r & 1) ? (gridDim.x - 1 - blockIdx.x) : blockIdx.x);
   return u < n_work ? u : -1;
-}
-
-// ------------------------------------------------------------------ statistics
-__global__ void __launch_bounds__(256) dense_stat_kernel(const DenseArgs a) {
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= (long long)a.nq * a.H) return;
-  const uint2 x = reinterpret_cast<const uint2 *>(a.out + w * kHeadDim)[lane];
-  const uint2 y = reinterpret_cast<const uint2 *>(a.dout + w * kHeadDim)[lane];
-  float s = bf16_lo(x.x) * bf16_lo(y.x);
-  s = fmaf(bf16_hi(x.x), bf16_hi(y.x), s);
-  s = fmaf(bf16_lo(x.y), bf16_lo(y.y), s);
-  s = fmaf(bf16_hi(x.y), bf16_hi(y.y), s);
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (lane == 0) a.stat[w] = make_float2(-a.lse[w] * 1.4426950408889634f, -s);
 }
 
 // ------------------------------------------------------------------ dk, dv
@@ -737,14 +722,8 @@ cudaError_t launch_bwd_r(const CUtensorMap &tq, const CUtensorMap &tdo, const CU
 cudaError_t launch_dense_varlen_backward(const CUtensorMap &tq, const CUtensorMap &tdo, const CUtensorMap &tk,
                                          const CUtensorMap &tv, const DenseArgs &a, int num_sms,
                                          cudaStream_t st) {
-  cudaError_t e = launch_dense_plan(a, 128 / (a.H / a.G), st);
+  cudaError_t e = launch_dense_plan(a, 128 / (a.H / a.G), num_sms, st);
   if (e != cudaSuccess) return e;
-  if (a.nq > 0) {
-    const long long rows = (long long)a.nq * a.H;
-    dense_stat_kernel<<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
   switch (a.H / a.G) {
     case 1: return launch_bwd_r<1>(tq, tdo, tk, tv, a, num_sms, st);
     case 2: return launch_bwd_r<2>(tq, tdo, tk, tv, a, num_sms, st);

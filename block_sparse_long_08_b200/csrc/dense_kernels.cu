@@ -22,7 +22,8 @@
 // 32K tokens, 8 heads on 1 KV head 1.94 ms (1136 TFLOP/s, 0.69 of burst
 // bf16).  Tried and slower: a quarter to half of the exponentials as
 // polynomials on the FMA pipe (1.98 ms at a quarter: an FMA pair takes two
-// issue slots), two softmax warpgroups per tile, an issuer per tile (the
+// issue slots), P handed over in halves (1.81 ms against 1.70 on one GPU: the
+// issuer then waits inside a tile), two softmax warpgroups per tile, an issuer per tile (the
 // products of both then finish late), S held back to interleave it with the
 // other tile's O (the tiles fall into step: 3.2 ms).
 //
@@ -84,12 +85,48 @@ __device__ __forceinline__ int block_exclusive(int v, int *s_warp, int &total) {
   return inc - v + (warp ? s_warp[warp - 1] : 0);
 }
 
+// {-lse log2 e, -D} of rows row0 .. (D = dout . out), two rows per warp and
+// step, 16 bytes of out and of dout per lane; two steps' loads are in flight.
+__device__ __forceinline__ void row_stats(const DenseArgs &a, long long first, long long stride, int lane) {
+  const long long rows = (long long)a.nq * a.H;
+  const int half = lane >> 4;
+  for (long long r0 = first * 4; r0 < rows; r0 += stride * 4) {
+    uint4 x[2], y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long r = min(r0 + 2 * i + half, rows - 1);
+      x[i] = reinterpret_cast<const uint4 *>(a.out + r * kHeadDim)[lane & 15];
+      y[i] = reinterpret_cast<const uint4 *>(a.dout + r * kHeadDim)[lane & 15];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(bf16_lo(xs[e]), bf16_lo(ys[e]), s);
+        s = fmaf(bf16_hi(xs[e]), bf16_hi(ys[e]), s);
+      }
+#pragma unroll
+      for (int m = 8; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      const long long r = r0 + 2 * i + half;
+      if ((lane & 15) == 0 && r < rows) a.stat[r] = make_float2(-a.lse[r] * 1.4426950408889634f, -s);
+    }
+  }
+}
+
 // One CTA per list: the items of `per` queries (block 0) and the key tiles of
-// 128 keys (block 1, for the backward).  Items are sorted by their number of
+// 128 keys (block 1, for the backward); the other blocks make the backward's
+// row statistics meanwhile.  Items are sorted by their number of
 // key tiles (query tiles of qpi queries), in at most 1024 steps of equal
 // width (a counting sort; the order inside a step does not matter, an item's
 // result depends on nothing but the item).
 __global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int per, int qpi) {
+  if (blockIdx.x > 1) {
+    row_stats(a, (long long)(blockIdx.x - 2) * 32 + (threadIdx.x >> 5), (long long)(gridDim.x - 2) * 32,
+              threadIdx.x & 31);
+    return;
+  }
   const bool keys = blockIdx.x == 1;
   int *prefix = keys ? a.prefix_k : a.prefix;
   int2 *items = keys ? a.items_k : a.items;
@@ -625,14 +662,19 @@ cudaError_t launch_fwd_r(const CUtensorMap &tq, const CUtensorMap &tk, const CUt
 
 }  // namespace
 
-cudaError_t launch_dense_plan(const DenseArgs &a, int per, cudaStream_t st) {
-  dense_plan_kernel<<<a.items_k ? 2 : 1, 1024, 0, st>>>(a, per, 128 / (a.H / a.G));
+cudaError_t launch_dense_plan(const DenseArgs &a, int per, int num_sms, cudaStream_t st) {
+  int grid = 1;
+  if (a.items_k) {   // the backward: the key tiles' list, and the rows' statistics
+    const long long blocks = ((long long)a.nq * a.H + 127) / 128;
+    grid = 2 + int(blocks < 2 * num_sms ? blocks : 2 * num_sms);
+  }
+  dense_plan_kernel<<<grid, 1024, 0, st>>>(a, per, 128 / (a.H / a.G));
   return cudaGetLastError();
 }
 
 cudaError_t launch_dense_varlen(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                 const DenseArgs &a, int num_sms, cudaStream_t st) {
-  cudaError_t e = launch_dense_plan(a, dense_item_queries(a.H / a.G), st);
+  cudaError_t e = launch_dense_plan(a, dense_item_queries(a.H / a.G), num_sms, st);
   if (e != cudaSuccess) return e;
   switch (a.H / a.G) {
     case 1: return launch_fwd_r<1>(tq, tk, tv, a, num_sms, st);
