@@ -54,4 +54,46 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Four 16-byte granules per lane, transposed among the lanes of a quad: lane
+// l's granule j becomes lane j's granule l.
+__device__ __forceinline__ void quad_transpose(uint4 (&g)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+      uint4 &lo = g[i], &hi = g[i | bit];
+      uint4 t = up ? lo : hi;
+      t.x = __shfl_xor_sync(0xffffffffu, t.x, bit);
+      t.y = __shfl_xor_sync(0xffffffffu, t.y, bit);
+      t.z = __shfl_xor_sync(0xffffffffu, t.z, bit);
+      t.w = __shfl_xor_sync(0xffffffffu, t.w, bit);
+      if (up) lo = t; else hi = t;
+    }
+  }
+}
+// 32 fp32 values of this lane's row times f, as bf16, to granules g0 .. g0+3 of
+// the row.  A lane per row would touch 32 lines with every store, 16 bytes
+// of each; the quad's transpose makes it eight lines, 64 bytes of each.
+// row_ptr(j): where row j of the quad's four (tile rows row & ~3 ..) begins,
+// or null when it is not to be written.  All lanes of the warp take part.
+template <typename RowPtr>
+__device__ __forceinline__ void quad_store32(const float *v, float f, int g0, RowPtr row_ptr) {
+  uint4 g[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    g[c] = make_uint4(pack_bf16x2(v[8 * c] * f, v[8 * c + 1] * f), pack_bf16x2(v[8 * c + 2] * f, v[8 * c + 3] * f),
+                      pack_bf16x2(v[8 * c + 4] * f, v[8 * c + 5] * f),
+                      pack_bf16x2(v[8 * c + 6] * f, v[8 * c + 7] * f));
+  quad_transpose(g);
+  const int l = threadIdx.x & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint16_t *p = row_ptr(j);
+    if (p) reinterpret_cast<uint4 *>(p)[g0 + l] = g[j];
+  }
+}
+
 }  // namespace msa

@@ -100,14 +100,6 @@ __device__ __forceinline__ void store64(uint32_t taddr, const float (&v)[64]) {
   tmem_st32u(taddr, w);
   tmem_wait_st();
 }
-// 64 values times f as bf16 into one row's 128 bytes.
-__device__ __forceinline__ void put64(uint16_t *dst, const float (&v)[64], float f) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    reinterpret_cast<uint4 *>(dst)[c] =
-        make_uint4(pack_bf16x2(v[8 * c] * f, v[8 * c + 1] * f), pack_bf16x2(v[8 * c + 2] * f, v[8 * c + 3] * f),
-                   pack_bf16x2(v[8 * c + 4] * f, v[8 * c + 5] * f), pack_bf16x2(v[8 * c + 6] * f, v[8 * c + 7] * f));
-}
 __device__ __forceinline__ void load_tile(uint32_t dst, const void *tm, uint32_t bar, int y, int z) {
   tma_load_3d(dst, tm, bar, 0, y, z);
   tma_load_3d(dst + 16384, tm, bar, 64, y, z);
@@ -429,13 +421,21 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       ++it;
       tc_fence_after();
-      float x[64];
-      load64(tl + kVTmDV + hc * 64, x);
-      if (key < w.keys) put64(dv, x, 1.f);
-      load64(tl + kVTmDK + hc * 64, x);
-      tc_fence_before();
-      mbar_arrive(bar(kVAccEmpty));
-      if (key < w.keys) put64(dk, x, a.scale);
+      const size_t row4 = size_t(w.key0 + (key & ~3)) * a.G + w.g;   // the quad's first key
+      const int left = w.keys - (key & ~3);
+#pragma unroll 1
+      for (int m = 0; m < 2; ++m) {
+        float x[64];
+        load64(tl + (m ? kVTmDK : kVTmDV) + hc * 64, x);
+        if (m) {
+          tc_fence_before();
+          mbar_arrive(bar(kVAccEmpty));
+        }
+        uint16_t *out = (m ? a.dk : a.dv) + row4 * kHeadDim;
+        auto ptr = [&](int j) { return j < left ? out + size_t(j) * a.G * kHeadDim : nullptr; };
+        quad_store32(x, m ? a.scale : 1.f, hc * 8, ptr);
+        quad_store32(x + 32, m ? a.scale : 1.f, hc * 8 + 4, ptr);
+      }
     }
   }
   tc_fence_before();
@@ -691,7 +691,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
       load64(tl + kGTmDQ + hc * 64, x);
       tc_fence_before();
       mbar_arrive(bar(kGAccEmpty));
-      if (valid) put64(dq, x, a.scale);
+      auto ptr = [&](int j) {
+        const int rw = (row & ~3) + j, i = rw / R;
+        return i < w.n ? a.dq + (size_t(w.q0 + i) * a.H + w.g * R + rw % R) * kHeadDim : nullptr;
+      };
+      quad_store32(x, a.scale, hc * 8, ptr);
+      quad_store32(x + 32, a.scale, hc * 8 + 4, ptr);
     }
   }
   tc_fence_before();

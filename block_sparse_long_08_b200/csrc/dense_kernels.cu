@@ -267,12 +267,6 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// One 16-byte store of eight fp32 values times f as bf16.
-__device__ __forceinline__ uint4 pack8_scaled(const float *x, float f) {
-  return make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
-                    pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f));
-}
-
 template <int R>
 __global__ void __launch_bounds__(kFThreads, 1)
     dense_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -620,10 +614,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
           float o[32];
           tmem_ld32(tm_lane + kFTmO + x * 128 + c * 32, o);
           tmem_wait_ld();
-          if (valid) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[4 * c + e] = pack8_scaled(o + 8 * e, inv);
-          }
+          quad_store32(o, inv, 4 * c, [&](int j) {
+            const int rw = (row & ~3) + j, i = x * QPI + rw / R;
+            return i < w.n ? a.out + (size_t(w.q0 + i) * a.H + w.g * R + rw % R) * kHeadDim : nullptr;
+          });
         }
         tc_fence_before();
         mbar_arrive(bar(kFOEmpty + x));
