@@ -286,3 +286,45 @@ def test_prompt_then_steps_equal_the_whole_sequence(fp8):
         p = prompts[b]
         assert np.linalg.norm(err[:p]) <= 1.2e-2 * np.linalg.norm(ref[:p])
         assert np.linalg.norm(err[p:]) <= (0.12 if fp8 else 1.2e-2) * np.linalg.norm(ref[p:])
+
+
+def test_rows_behind_two_billion_values():
+    """Packed rows whose element offsets pass 2^31: sequences at the end give
+    what they give alone."""
+    H, G, n, B = 64, 4, 128, 2080
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    lens = [n] * (B - 1) + [77]
+    cu = [0] + np.cumsum(lens).tolist()
+    q, dout = (torch.randn(cu[-1], H, 128, device=DEV, dtype=BF16, generator=gen) for _ in range(2))
+    k, v = (torch.randn(cu[-1], G, 128, device=DEV, dtype=BF16, generator=gen) for _ in range(2))
+    assert q.numel() > 2 ** 31
+    out, lse = M.msa_dense_attn_varlen(q, k, v, i32(cu), i32(cu), want_lse=True)
+    g = M.msa_dense_attn_varlen_backward(q, k, v, out, lse, dout, i32(cu), i32(cu))
+    for b in (0, 1000, B - 2, B - 1):
+        s = slice(cu[b], cu[b + 1])
+        c = [0, lens[b]]
+        o, ls = M.msa_dense_attn_varlen(q[s], k[s], v[s], i32(c), i32(c), want_lse=True)
+        assert torch.equal(o, out[s]) and torch.equal(ls, lse[s]), b
+        h = M.msa_dense_attn_varlen_backward(q[s], k[s], v[s], o, ls, dout[s], i32(c), i32(c))
+        assert all(torch.equal(x, y[s]) for x, y in zip(h, g)), b
+
+
+def test_many_sequences_and_more_than_the_plan_holds_at_once():
+    """3000 sequences of 0 to 5 tokens: the plan walks them in chunks."""
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 6, 3000).tolist()
+    x, cq, ck = packed(lens, lens, 1, 4, seed=9, tail=3)
+    out, lse = run(x, cq, ck)
+    check_forward(x, cq, ck, out, lse)
+    check_backward(x, cq, ck, out, lse)
+
+
+def test_forward_without_lse_and_on_a_given_stream():
+    lens = [200, 90]
+    x, cq, ck = packed(lens, lens, 2, 4, seed=10)
+    want, _ = run(x, cq, ck)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = M.msa_dense_attn_varlen(x["q"], x["k"], x["v"], i32(cq), i32(ck), stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)

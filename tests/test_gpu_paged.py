@@ -294,3 +294,116 @@ def test_append_bad_input_is_skipped():
     assert call([3, 9], [0, 3, 9], good)[0] == bad                             # more rows than given
     assert call([3, 3], [3, 0, 6], good)[0] == bad                             # descending
     assert call([-3, 3], [0, 3, 6], good) == (bad, [[1, 0], [1, 1], [1, 2]])
+
+
+# ------------------------------------------------------------ together, in use
+
+def test_captured_step_serves_other_lengths_and_pages():
+    """One captured append + decode step replays with other lengths, pages and
+    values; a padding sequence joins in."""
+    B, G, R, page, cols = 4, 2, 4, 16, 20
+    gen = torch.Generator().manual_seed(21)
+    kp, vp = (torch.randn(B * cols, page, G, 128, generator=gen).to(BF16).to(DEV) for _ in range(2))
+    table = torch.arange(B * cols, dtype=torch.int32).reshape(B, cols).to(DEV)
+    lens = torch.tensor([5, 17, 300, 0], dtype=torch.int32, device=DEV)
+    q, k, v = (torch.randn(B, h, 128, generator=gen).to(BF16).to(DEV) for h in (G * R, G, G))
+    f = (10000.0 ** (-torch.arange(64).float() / 64)).to(DEV)
+    wa = M.new_paged_workspace(M.MSA_OP_PAGED_APPEND, table, page, G * R, G)
+    wd = M.new_paged_workspace(M.MSA_OP_PAGED_DECODE, table, page, G * R, G)
+    qo, out = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.zeros(B, G * R, device=DEV)
+
+    def step():
+        M.msa_paged_append(k, v, kp, vp, table, lens, q=q, q_out=qo, inv_freq=f, ws=wa)
+        M.msa_paged_attn_decode(qo, kp, vp, table, lens, out=out, lse=lse, ws=wd)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    for n in ([5, 17, 300, 0], [320, 1, 0, 16], [31, 32, 33, 257]):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=gen).to(BF16))
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        table.copy_(torch.randperm(B * cols, generator=gen).to(torch.int32).reshape(B, cols))
+        kc, vc = kp.clone(), vp.clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        qe = torch.zeros_like(q)
+        qe[:] = qo                                # (a padding row keeps what it held)
+        M.msa_paged_append(k, v, kc, vc, table, lens, q=q, q_out=qe, inv_freq=f)
+        assert torch.equal(kc, kp) and torch.equal(vc, vp) and torch.equal(qe, qo)
+        c = {"table": table, "k": kp, "v": vp, "ks": None, "vs": None}
+        check_decode(c, qo, n, out, lse)
+    assert M.msa_read_status(wa) == M.MSA_OK and M.msa_read_status(wd) == M.MSA_OK
+
+
+def test_two_streams_at_once_with_their_own_workspaces():
+    lens = [4000, 1, 900, 2500]
+    c = make_cache(lens, 4, 64, False, seed=31)
+    q = torch.randn(4, 16, 128, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV)
+    t = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = M.msa_paged_attn_decode(q, c["k"], c["v"], c["table"], t)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [M.new_paged_workspace(M.MSA_OP_PAGED_DECODE, c["table"], 64, 16, 4) for _ in range(2)]
+    outs = [[torch.zeros_like(q) for _ in range(20)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for x, s in enumerate(streams):
+            M.msa_paged_attn_decode(q, c["k"], c["v"], c["table"], t, out=outs[x][i], ws=ws[x], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for x in outs for o in x)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_behind_four_billion_values(fp8):
+    """A pool of more than 2^32 values: the last pages are written and read."""
+    G, page, H = 8, 256, 16
+    num = (1 << 32) // (page * G * 128) + 9
+    kind = torch.uint8 if fp8 else BF16
+    kp, vp = (torch.zeros(num, page, G, 128, dtype=kind, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros(num, page, G, device=DEV) if fp8 else None for _ in range(2))
+    small = [torch.zeros(9, page, G, 128, dtype=kind, device=DEV) for _ in range(2)]
+    ss = [torch.zeros(9, page, G, device=DEV) if fp8 else None for _ in range(2)]
+    n = 700
+    gen = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(n, G, 128, generator=gen).to(BF16).to(DEV) for _ in range(2))
+    q = torch.randn(1, H, 128, generator=gen).to(BF16).to(DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    outs = []
+    for a, b, sa, sb, first in ((kp, vp, ks, vs, num - 9), (*small, *ss, 0)):
+        table = torch.tensor([[first + 8, first + 3, first + 5]], dtype=torch.int32, device=DEV)
+        M.msa_paged_append(k, v, a, b, table, lens, cu_new=cu, k_scale=sa, v_scale=sb)
+        outs.append(M.msa_paged_attn_decode(q, a, b, table, lens, k_scale=sa, v_scale=sb))
+    torch.cuda.synchronize()
+    assert torch.equal(kp[num - 9:], small[0]) and torch.equal(vp[num - 9:], small[1])
+    assert not kp[:16].any()
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("scales", ["wide", "signed", "zero"])
+def test_decode_fp8_scales_of_any_size(scales):
+    """Scales from 1e-12 to 1e12 beside each other, negative ones, zeros."""
+    lens = [300, 33]
+    c = make_cache(lens, 2, 16, True, seed=41)
+    gen = torch.Generator().manual_seed(5)
+    s = torch.rand(c["vs"].shape, generator=gen) + 0.5
+    if scales == "wide":
+        s = s * 10.0 ** (24 * torch.rand(s.shape, generator=gen) - 12)
+    elif scales == "signed":
+        s = s * (2 * torch.randint(0, 2, s.shape, generator=gen) - 1)
+    else:
+        s = s * torch.randint(0, 2, s.shape, generator=gen)
+    c["vs"] = torch.where(c["own"][..., None].to(DEV), s.to(DEV), float("nan"))
+    q = torch.randn(2, 16, 128, generator=gen).to(BF16).to(DEV)
+    out, lse = decode(c, q, lens)
+    check_decode(c, q, lens, out, lse)
+    if scales == "zero":
+        c["vs"] = torch.where(c["own"][..., None].to(DEV), torch.zeros_like(c["vs"]), float("nan"))
+        out, _ = decode(c, q, lens)
+        assert (out == 0).all()
