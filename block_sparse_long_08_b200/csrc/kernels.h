@@ -258,6 +258,7 @@ struct DenseArgs {
   int2 *items;                 // {sequence, query item}, longest first
   int *n_items;
   int max_items;               // entries of `items`
+  int fused;                   // forward of a small call: no lists, every CTA plans for itself
   // the backward's: key tiles of 128 keys, most query tiles first, and
   // {-lse log2 e, -dout . out} of every (query row, head)
   int *prefix_k;

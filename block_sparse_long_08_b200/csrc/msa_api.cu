@@ -770,6 +770,7 @@ int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa
   a->items = reinterpret_cast<int2 *>(wsb + w.items);
   const int r = p->H / p->G;
   a->max_items = msa::dense_max_items(nq, backward ? 128 / r : msa::dense_item_queries(r), p->B);
+  a->fused = 0;
   a->prefix_k = nullptr; a->items_k = nullptr; a->n_items_k = nullptr; a->stat = nullptr;
   a->max_items_k = 0;
   if (backward) {

@@ -760,24 +760,20 @@ def _stream_on(stream, dev):
     return _stream(stream)
 
 
-class _on_device:
-    """The call's device as the current one (streams, launches and the SM
-    count the library asks for belong to the device of the tensors)."""
+def _launch(fn, dev, *args):
+    """The call, with the tensors' device as the current one (streams, launches
+    and the SM count the library asks for belong to it)."""
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    else:
+        rc = fn(*args)
+    if rc != MSA_OK:
+        raise MSAError(rc, msa_last_error())
 
-    __slots__ = ("want", "back")
 
-    def __init__(self, dev):
-        self.want = dev.index if dev.type == "cuda" else None
-
-    def __enter__(self):
-        self.back = None
-        if self.want is not None and torch.cuda.current_device() != self.want:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.want)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _dense_params(B, L, H, G, d, scale=0.0):
+    return msa_params(B, L, H, G, d, 128, 128, 16, scale, 0)
 
 
 def _call_ws(ws, p, op, dev):
@@ -858,12 +854,10 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
     cu = None if cu_new is None else _fits(cu_new, "cu_new", _I32, B + 1, dev)
     fa = _fits(inv_freq, "inv_freq", _F32, rot_dim // 2, dev) if rot_dim else None
     ko = None if k_out is None else _fits(k_out, "k_out", _BF16, kv, dev)
-    p = make_params(B, L, H, G, d)
-    with _on_device(dev):
-        ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_APPEND, dev)
-        _check(lib().msa_paged_append(ctypes.byref(p), ctypes.byref(c), N, qa, k.data_ptr(), va, cu, la,
-                                      fa, int(rot_dim), int(bool(interleaved)), qo, ko, wa, wn,
-                                      _stream_on(stream, dev)))
+    p = _dense_params(B, L, H, G, d)
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_APPEND, dev)
+    _launch(lib().msa_paged_append, dev, ctypes.byref(p), ctypes.byref(c), N, qa, k.data_ptr(), va, cu,
+            la, fa, int(rot_dim), int(bool(interleaved)), qo, ko, wa, wn, _stream_on(stream, dev))
     return q_out
 
 
@@ -886,11 +880,10 @@ def msa_paged_attn_decode(q, k_pages, v_pages, page_table, seq_lens, *, k_scale=
     if lse is None and want_lse:
         lse = torch.empty((B, H), dtype=_F32, device=dev)
     ea = None if lse is None else _fits(lse, "lse", _F32, B * H, dev)
-    p = make_params(B, L, H, G, d, scale=scale)
-    with _on_device(dev):
-        ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_DECODE, dev)
-        _check(lib().msa_paged_attn_decode(ctypes.byref(p), ctypes.byref(c), q.data_ptr(), la, oa, ea,
-                                           wa, wn, _stream_on(stream, dev)))
+    p = _dense_params(B, L, H, G, d, scale)
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_DECODE, dev)
+    _launch(lib().msa_paged_attn_decode, dev, ctypes.byref(p), ctypes.byref(c), q.data_ptr(), la, oa, ea,
+            wa, wn, _stream_on(stream, dev))
     return (out, lse) if lse is not None else out
 
 
@@ -904,7 +897,7 @@ def _dense_inputs(q, k, v, cu_q, cu_k, scale):
         raise ValueError("cu_q needs one entry more than there are sequences")
     adr = (q.data_ptr(), _fits(k, "k", _BF16, nk * G * d, dev), _fits(v, "v", _BF16, nk * G * d, dev))
     cus = (_fits(cu_q, "cu_q", _I32, 0, dev), _fits(cu_k, "cu_k", _I32, B + 1, dev))
-    return nq, nk, make_params(B, max(nq, nk), H, G, d, scale=scale), adr, cus, dev
+    return nq, nk, _dense_params(B, max(nq, nk), H, G, d, scale), adr, cus, dev
 
 
 def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: bool = False,
@@ -920,10 +913,9 @@ def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: 
     if lse is None and want_lse:
         lse = torch.empty((nq, H), dtype=_F32, device=dev)
     ea = None if lse is None else _fits(lse, "lse", _F32, nq * H, dev)
-    with _on_device(dev):
-        ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN, dev)
-        _check(lib().msa_dense_attn_varlen(ctypes.byref(p), nq, nk, *adr, *cus, oa, ea, wa, wn,
-                                           _stream_on(stream, dev)))
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN, dev)
+    _launch(lib().msa_dense_attn_varlen, dev, ctypes.byref(p), nq, nk, *adr, *cus, oa, ea, wa, wn,
+            _stream_on(stream, dev))
     return (out, lse) if lse is not None else out
 
 
@@ -939,10 +931,9 @@ def msa_dense_attn_varlen_backward(q, k, v, out, lse, dout, cu_q, cu_k, *, scale
     oa, da, qa = (_fits(t, n, _BF16, q.numel(), dev) for n, t in (("out", out), ("dout", dout), ("dq", dq)))
     ka, va = (_fits(t, n, _BF16, nkv, dev) for n, t in (("dk", dk), ("dv", dv)))
     ea = _fits(lse, "lse", _F32, nq * q.shape[1], dev)
-    with _on_device(dev):
-        ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, dev)
-        _check(lib().msa_dense_attn_varlen_backward(ctypes.byref(p), nq, nk, *adr, oa, ea, da, *cus, qa,
-                                                    ka, va, wa, wn, _stream_on(stream, dev)))
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, dev)
+    _launch(lib().msa_dense_attn_varlen_backward, dev, ctypes.byref(p), nq, nk, *adr, oa, ea, da, *cus,
+            qa, ka, va, wa, wn, _stream_on(stream, dev))
     return dq, dk, dv
 
 
