@@ -217,9 +217,14 @@ struct PdCfg {
   // a stage: 16 K rows and 16 V rows (8-bit: and their scales)
   static constexpr int KB = 16 * kHeadDim * (FP8 ? 1 : 2);
   static constexpr int STAGE = 2 * KB + (FP8 ? 128 : 0);
+  // An 8-bit cache's limit is the warps' instructions (codes to f16); with up
+  // to eight heads the products run with the keys as the 16 rows and the
+  // heads as the 8 columns, half as many of them, and V's codes go from their
+  // rows into fragments without a detour through shared memory.
+  static constexpr bool KM = FP8 && R <= 8;
   static constexpr int NST = 3;
   static constexpr int CTAS = FP8 ? 3 : 2;   // per SM (8 bits: 3 measured 413 us, 2 438 us on 96 x <= 16K tokens)
-  static constexpr int SCR = FP8 ? 4096 : 0;   // a step's V rows as bf16
+  static constexpr int SCR = FP8 && !KM ? 4096 : 0;   // a step's V rows as bf16
   static constexpr int WARP = NST * STAGE + SCR;
   static constexpr int OFF_O = 4 * WARP;       // [R][128] fp32
   static constexpr int OFF_ML = OFF_O + R * kHeadDim * 4;   // [4][16] maxima, [4][16] sums
@@ -281,11 +286,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // Byte of 16-byte granule gr of row r in a stage: rows of 256 bytes (8-bit:
-// 128), granules permuted so that eight rows of one granule (8-bit: two rows
-// of four granules) fall into different banks.
+// 128), granules permuted so that eight rows of one granule (8-bit: two
+// neighbouring rows of four granules, and four even or odd rows of two) fall
+// into different banks.
 template <bool FP8>
 __device__ __forceinline__ uint32_t swz(int r, int gr) {
-  return FP8 ? r * 128 + ((gr ^ ((r & 1) << 2)) << 4) : r * 256 + ((gr ^ (r & 7)) << 4);
+  return FP8 ? r * 128 + ((gr ^ (((r & 6) ^ ((r & 1) << 2)))) << 4) : r * 256 + ((gr ^ (r & 7)) << 4);
+}
+// An 8 x 8 matrix of 16-bit values (row lane / 4, columns 2 (lane % 4), + 1) transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // The fp32 at this CTA's shared address `a` in CTA `rank` of the cluster.
@@ -460,9 +472,11 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
 
     // running state of the pair: rows g4 and g4 + 8 of the 16 head rows
     // (8-bit: O is kept against mw, the others against m)
-    float o[16][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, mw0 = -INFINITY, mw1 = -INFINITY;
+    // (KM: heads 2c and 2c + 1 in place of rows g4 and g4 + 8; O's value e of
+    // tile d is dim 16 g4 + 2 d + e / 2 of head 2c + e % 2)
+    float o[C::KM ? 8 : 16][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, mw0 = -INFINITY, mw1 = -INFINITY;
 #pragma unroll
-    for (int d = 0; d < 16; ++d)
+    for (int d = 0; d < (C::KM ? 8 : 16); ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     uint32_t qf[8][4];
@@ -478,6 +492,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            if (C::KM && (e & 1)) continue;   // the B operand's two registers: e 0 and 2
             const int r = g4 + (e & 1) * 8;
             // bf16: dims 16 kk + 2c, +1 (e < 2) and + 8; 8-bit: the order in
             // which a lane's sixteen codes of a granule feed four k steps
@@ -491,7 +506,88 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
       __syncwarp();
       const int vis = s_vis[st];
       const uint32_t kb = sm + st * C::STAGE, vb = kb + C::KB;
-      if (vis > 0) {
+      if (C::KM && vis > 0) {
+        const uint8_t *ks = smp + st * C::STAGE;
+        const float *sc = reinterpret_cast<const float *>(ks + 2 * C::KB);
+        // S^T: rows are keys g4 and g4 + 8, columns heads 2c and 2c + 1
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 u0 = *reinterpret_cast<const uint4 *>(ks + swz<true>(g4, c + 4 * h));
+          const uint4 u1 = *reinterpret_cast<const uint4 *>(ks + swz<true>(g4 + 8, c + 4 * h));
+          const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t ka[4] = {f16x2_of_e4m3x2(w0[x]), f16x2_of_e4m3x2(w1[x]), f16x2_of_e4m3x2(w0[x] >> 16),
+                                    f16x2_of_e4m3x2(w1[x] >> 16)};
+            mma_f16(s, ka, qf[4 * h + x][0], qf[4 * h + x][2]);
+          }
+        }
+        const float k0 = sc[g4] * a.scale_log2, k1 = sc[g4 + 8] * a.scale_log2;
+        const float v0 = sc[16 + g4], v1 = sc[24 + g4];
+        s[0] *= k0; s[1] *= k0; s[2] *= k1; s[3] *= k1;     // log2 units
+        if (vis < 16) {
+          if (g4 >= vis) s[0] = s[1] = -INFINITY;
+          if (g4 + 8 >= vis) s[2] = s[3] = -INFINITY;
+        }
+        const float lv0 = __log2f(fabsf(v0)), lv1 = __log2f(fabsf(v1));
+        float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+        float y0 = fmaxf(s[0] + lv0, s[2] + lv1), y1 = fmaxf(s[1] + lv0, s[3] + lv1);
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, i));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, i));
+          y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, i));
+          y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, i));
+        }
+        // two references as below: m for the sums, mw for the weights that
+        // multiply V's codes (P |scale|, f16); both in log2 units here
+        const bool u0 = m0 == -INFINITY || x0 - m0 > 8.f, u1 = m1 == -INFINITY || x1 - m1 > 8.f;
+        const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > 8.f);
+        const bool wu1 = y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > 8.f);
+        if (__any_sync(0xffffffffu, u0 || u1 || wu0 || wu1)) {
+          if (u0) { l0 *= m0 == -INFINITY ? 0.f : exp2_fast(m0 - x0); m0 = x0; }
+          if (u1) { l1 *= m1 == -INFINITY ? 0.f : exp2_fast(m1 - x1); m1 = x1; }
+          const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - y0)) : 1.f;
+          const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - y1)) : 1.f;
+          if (wu0) mw0 = y0;
+          if (wu1) mw1 = y1;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            o[d][0] *= al0; o[d][2] *= al0;
+            o[d][1] *= al1; o[d][3] *= al1;
+          }
+        }
+        l0 += exp2_fast(s[0] - m0) + exp2_fast(s[2] - m0);
+        l1 += exp2_fast(s[1] - m1) + exp2_fast(s[3] - m1);
+        const float n0 = mw0 == -INFINITY ? 0.f : -mw0, n1 = mw1 == -INFINITY ? 0.f : -mw1;
+        const __half2 p0 = __floats2half2_rn(copysignf(exp2_fast(s[0] + lv0 + n0), v0),
+                                             copysignf(exp2_fast(s[1] + lv0 + n1), v0));
+        const __half2 p1 = __floats2half2_rn(copysignf(exp2_fast(s[2] + lv1 + n0), v1),
+                                             copysignf(exp2_fast(s[3] + lv1 + n1), v1));
+        const uint32_t b0 = transpose8(*reinterpret_cast<const uint32_t *>(&p0));
+        const uint32_t b1 = transpose8(*reinterpret_cast<const uint32_t *>(&p1));
+        // O^T += V^T P^T: this lane's dims are 16 g4 .. + 15 (rows g4 and g4 + 8
+        // of the eight tiles), its keys 2c, 2c + 1, 2c + 8, 2c + 9
+        const uint8_t *vr = ks + C::KB;
+        const uint4 q0 = *reinterpret_cast<const uint4 *>(vr + swz<true>(2 * c, g4));
+        const uint4 q1 = *reinterpret_cast<const uint4 *>(vr + swz<true>(2 * c + 1, g4));
+        const uint4 q2 = *reinterpret_cast<const uint4 *>(vr + swz<true>(2 * c + 8, g4));
+        const uint4 q3 = *reinterpret_cast<const uint4 *>(vr + swz<true>(2 * c + 9, g4));
+        const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
+        const uint32_t w2[4] = {q2.x, q2.y, q2.z, q2.w}, w3[4] = {q3.x, q3.y, q3.z, q3.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t e0 = __byte_perm(w0[j], w1[j], h ? 0x7362 : 0x5140);
+            const uint32_t e1 = __byte_perm(w2[j], w3[j], h ? 0x7362 : 0x5140);
+            const uint32_t va[4] = {f16x2_of_e4m3x2(e0), f16x2_of_e4m3x2(e0 >> 16), f16x2_of_e4m3x2(e1),
+                                    f16x2_of_e4m3x2(e1 >> 16)};
+            mma_f16(o[2 * j + h], va, b0, b1);
+          }
+      }
+      if (!C::KM && vis > 0) {
         float s[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -657,21 +753,26 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
       // ---- the pair's end, or the run's: join the four warps
       const bool done = --pair_left == 0;
       if (done || u + 1 == u1) {
+        const int h0 = C::KM ? 2 * c : g4, h1 = C::KM ? 2 * c + 1 : g4 + 8;   // this lane's heads
 #pragma unroll
-        for (int i = 1; i < 4; i <<= 1) {
+        for (int i = C::KM ? 4 : 1; i < (C::KM ? 32 : 4); i <<= 1) {
           l0 += __shfl_xor_sync(0xffffffffu, l0, i);
           l1 += __shfl_xor_sync(0xffffffffu, l1, i);
         }
-        if (c == 0) {
-          s_m[warp * 16 + g4] = m0; s_m[warp * 16 + g4 + 8] = m1;
-          s_l[warp * 16 + g4] = l0; s_l[warp * 16 + g4 + 8] = l1;
+        if (C::KM) {   // from log2 units back to those of the scores
+          m0 /= a.scale_log2;
+          m1 /= a.scale_log2;
+        }
+        if (C::KM ? g4 == 0 : c == 0) {
+          s_m[warp * 16 + h0] = m0; s_m[warp * 16 + h1] = m1;
+          s_l[warp * 16 + h0] = l0; s_l[warp * 16 + h1] = l1;
         }
         __syncthreads();
         float M0 = -INFINITY, M1 = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          M0 = fmaxf(M0, s_m[w * 16 + g4]);
-          M1 = fmaxf(M1, s_m[w * 16 + g4 + 8]);
+          M0 = fmaxf(M0, s_m[w * 16 + h0]);
+          M1 = fmaxf(M1, s_m[w * 16 + h1]);
         }
         // O's unit, 2^(scale m) (8-bit: 2^mw), to 2^(scale M)
         const float u0 = FP8 ? mw0 : m0 * a.scale_log2, u1 = FP8 ? mw1 : m1 * a.scale_log2;
@@ -679,7 +780,21 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         const float f1 = u1 == -INFINITY ? 0.f : exp2_fast(u1 - M1 * a.scale_log2);
         // warp by warp, so that the sum's order is always the same
         for (int w = 0; w < 4; ++w) {
-          if (w == warp) {
+          if (C::KM && w == warp) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (2 * c + h >= R) continue;
+              float4 *x = reinterpret_cast<float4 *>(s_o + (2 * c + h) * kHeadDim + 16 * g4);
+              const float f = h ? f1 : f0;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                const float4 y = w ? x[d] : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[d] = make_float4(y.x + o[2 * d][h] * f, y.y + o[2 * d][2 + h] * f, y.z + o[2 * d + 1][h] * f,
+                                   y.w + o[2 * d + 1][2 + h] * f);
+              }
+            }
+          }
+          if (!C::KM && w == warp) {
 #pragma unroll
             for (int d = 0; d < 16; ++d) {
               if (g4 < R) {
@@ -727,7 +842,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         m0 = m1 = mw0 = mw1 = -INFINITY;
         l0 = l1 = 0.f;
 #pragma unroll
-        for (int d = 0; d < 16; ++d)
+        for (int d = 0; d < (C::KM ? 8 : 16); ++d)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
         fresh = true;
