@@ -217,7 +217,7 @@ constexpr int kFCtl = kFSKV + kFNkv * kFTile;
 // barriers
 constexpr int kFQFull = 0, kFQEmpty = 2, kFKvFull = 4, kFKvEmpty = 4 + kFNkv,
               kFSFull = 4 + 2 * kFNkv, kFPFull = kFSFull + 2, kFOFull = kFPFull + 2,
-              kFOEmpty = kFOFull + 2, kFLFull = kFOEmpty + 2, kFDrain = kFLFull + 2, kFVReq = kFDrain + 1, kFVClean = kFVReq + 1,
+              kFOEmpty = kFOFull + 2, kFLFull = kFOEmpty + 2, kFLEmpty = kFLFull + 2, kFDrain = kFLEmpty + 2, kFVReq = kFDrain + 1, kFVClean = kFVReq + 1,
               kFNumBars = kFVClean + 1;
 constexpr int kFCtlMisc = kFNumBars * 8;         // tmem holder, abort flag
 constexpr int kFCtlX = (kFCtlMisc + 8 + 15) & ~15;   // [2][128] row sums, [2][128] reference maxima
@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       mbar_init(bar(kFOFull + x), 1);
       mbar_init(bar(kFOEmpty + x), 128);
       mbar_init(bar(kFLFull + x), 128);
+      mbar_init(bar(kFLEmpty + x), 128);
     }
     for (int x = 0; x < kFNkv; ++x) {
       mbar_init(bar(kFKvFull + x), 1);
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const uint32_t tm_s = tm_lane + kFTmS + x * 128, tm_o = tm_lane + kFTmO + x * 128;
     const int qi = row / R;
     const float2 sc2 = f2_dup(a.scale_log2);
-    uint32_t sn = 0;
+    uint32_t sn = 0, ln = 0;
     bool ok = true;
     FItem w;
     for (int r = 0; ok && dense_item<R>(a, sm, r, n_work, w); ++r) {
@@ -614,8 +615,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
         mbar_arrive(bar(kFPFull + x));
       }
       if (!ok) break;
-      // the sum and the maximum go to the epilogue (which has read the last
-      // item's before it freed O, without which this item has no end)
+      // the sum and the maximum go to the epilogue, once it has read the last
+      // item's (this item's products may still wait for O then)
+      ok = mbar_wait(bar(kFLEmpty + x), ln ^ 1, abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ln ^= 1;
       s_l[x * 128 + row] = (l2.x + l3.x) + (l2.y + l3.y);
       s_m[x * 128 + row] = mr;
       mbar_arrive(bar(kFLFull + x));
@@ -649,6 +653,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         on ^= 1;
         const float l = s_l[x * 128 + row], mr = s_m[x * 128 + row];
+        mbar_arrive(bar(kFLEmpty + x));
         const float inv = l > 0.f ? 1.f / l : 0.f;
         tc_fence_after();
 #pragma unroll 1

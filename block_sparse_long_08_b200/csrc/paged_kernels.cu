@@ -223,7 +223,7 @@ struct PdCfg {
   // rows into fragments without a detour through shared memory.
   static constexpr bool KM = FP8 && R <= 8;
   static constexpr int NST = 3;
-  static constexpr int CTAS = FP8 ? 3 : 2;   // per SM (8 bits: 3 measured 413 us, 2 438 us on 96 x <= 16K tokens)
+  static constexpr int CTAS = KM ? 4 : FP8 ? 3 : 2;   // per SM (8-bit, 96 x <= 16K tokens: 4 321 us, 3 326 us)
   static constexpr int SCR = FP8 && !KM ? 4096 : 0;   // a step's V rows as bf16
   static constexpr int WARP = NST * STAGE + SCR;
   static constexpr int OFF_O = 4 * WARP;       // [R][128] fp32
