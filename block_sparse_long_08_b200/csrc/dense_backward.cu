@@ -210,12 +210,6 @@ __global__ void __launch_bounds__(kBThreads, 1)
       bool ok = true;
       for (int r = 0; ok && kv_item<R>(a, r, n_work, w); ++r) {
         if (w.n_qt == 0) continue;
-        ok = mbar_wait(bar(kVKvEmpty), (it & 1) ^ 1, abort_flag, a.status);
-        if (!ok) break;
-        mbar_arrive_expect_tx(bar(kVKvFull), 2 * kBTile);
-        load_tile(s_base + kBSKeep, &tm_k, bar(kVKvFull), w.g, w.key0);
-        load_tile(s_base + kBSKeep + kBTile, &tm_v, bar(kVKvFull), w.g, w.key0);
-        ++it;
         for (int i = 0; i < w.n_qt && ok; ++i, ++seq) {
           const int row = w.q0 + (w.qt0 + i) * QPI;
           ok = mbar_wait(bar(kVQEmpty + q.s), q.ph ^ 1, abort_flag, a.status);
@@ -229,6 +223,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
           mbar_arrive_expect_tx(bar(kVOFull + o.s), kBTile);
           load_tile(s_base + kBSShort + o.s * kBTile, &tm_do, bar(kVOFull + o.s), w.g * R, row);
           o.next(2);
+          if (i > 0) continue;
+          // K and V behind the first tiles: theirs are free only once the last
+          // item is done
+          ok = mbar_wait(bar(kVKvEmpty), (it & 1) ^ 1, abort_flag, a.status);
+          if (!ok) { ++seq; break; }
+          mbar_arrive_expect_tx(bar(kVKvFull), 2 * kBTile);
+          load_tile(s_base + kBSKeep, &tm_k, bar(kVKvFull), w.g, w.key0);
+          load_tile(s_base + kBSKeep + kBTile, &tm_v, bar(kVKvFull), w.g, w.key0);
+          ++it;
         }
       }
       // copies still in flight land before the CTA may exit
@@ -522,12 +525,6 @@ __global__ void __launch_bounds__(kBThreads, 1)
       bool ok = true;
       for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
         if (w.n_kt == 0) continue;
-        ok = mbar_wait(bar(kGQEmpty), (it & 1) ^ 1, abort_flag, a.status);
-        if (!ok) break;
-        mbar_arrive_expect_tx(bar(kGQFull), 2 * kBTile);
-        load_tile(s_base + kBSKeep, &tm_q, bar(kGQFull), w.g * R, w.q0);
-        load_tile(s_base + kBSKeep + kBTile, &tm_do, bar(kGQFull), w.g * R, w.q0);
-        ++it;
         for (int j = 0; j < w.n_kt && ok; ++j, ++seq) {
           ok = mbar_wait(bar(kGKEmpty + k.s), k.ph ^ 1, abort_flag, a.status);
           if (!ok) break;
@@ -540,6 +537,14 @@ __global__ void __launch_bounds__(kBThreads, 1)
           mbar_arrive_expect_tx(bar(kGVFull + v.s), kBTile);
           load_tile(s_base + kBSShort + v.s * kBTile, &tm_v, bar(kGVFull + v.s), w.g, w.key0 + j * 128);
           v.next(2);
+          if (j > 0) continue;
+          // Q and dO behind the first tiles (see above)
+          ok = mbar_wait(bar(kGQEmpty), (it & 1) ^ 1, abort_flag, a.status);
+          if (!ok) { ++seq; break; }
+          mbar_arrive_expect_tx(bar(kGQFull), 2 * kBTile);
+          load_tile(s_base + kBSKeep, &tm_q, bar(kGQFull), w.g * R, w.q0);
+          load_tile(s_base + kBSKeep + kBTile, &tm_do, bar(kGQFull), w.g * R, w.q0);
+          ++it;
         }
       }
       if (it) mbar_wait_drain(bar(kGQFull), (it - 1) & 1);

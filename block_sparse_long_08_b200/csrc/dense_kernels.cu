@@ -376,28 +376,31 @@ __global__ void __launch_bounds__(kFThreads, 1)
       FItem w;
       for (int r = 0; ok && dense_item<R>(a, sm, r, n_work, w); ++r) {
         const int n_kt = max(w.n_kt_a, w.n_kt_b);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || w.n_kt(x) == 0) continue;
-          ok = mbar_wait(bar(kFQEmpty + x), (qn[x] & 1) ^ 1, abort_flag, a.status);
-          if (!ok) continue;
-          mbar_arrive_expect_tx(bar(kFQFull + x), kFTile);
-          const uint32_t dst = s_base + kFSQ + x * kFTile;
-          tma_load_3d(dst, &tm_q, bar(kFQFull + x), 0, w.g * R, w.q0 + x * QPI);
-          tma_load_3d(dst + 16384, &tm_q, bar(kFQFull + x), 64, w.g * R, w.q0 + x * QPI);
-          ++qn[x];
-        }
         for (int step = 0; step < 2 * n_kt && ok; ++step) {
-          const int x = int(kseq % kFNkv);
-          ok = mbar_wait(bar(kFKvEmpty + x), ((kseq / kFNkv) & 1) ^ 1, abort_flag, a.status);
+          const int e = int(kseq % kFNkv);
+          ok = mbar_wait(bar(kFKvEmpty + e), ((kseq / kFNkv) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
-          mbar_arrive_expect_tx(bar(kFKvFull + x), kFTile);
+          mbar_arrive_expect_tx(bar(kFKvFull + e), kFTile);
           const void *tm = (step & 1) ? static_cast<const void *>(&tm_v) : static_cast<const void *>(&tm_k);
-          const uint32_t dst = s_base + kFSKV + x * kFTile;
+          const uint32_t dst = s_base + kFSKV + e * kFTile;
           const int key0 = w.k0 + (step >> 1) * 128;
-          tma_load_3d(dst, tm, bar(kFKvFull + x), 0, w.g, key0);
-          tma_load_3d(dst + 16384, tm, bar(kFKvFull + x), 64, w.g, key0);
+          tma_load_3d(dst, tm, bar(kFKvFull + e), 0, w.g, key0);
+          tma_load_3d(dst + 16384, tm, bar(kFKvFull + e), 64, w.g, key0);
           ++kseq;
+          if (step > 0) continue;
+          // Q behind the first K: its tiles are free only once the last item's
+          // scores are done
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || w.n_kt(x) == 0) continue;
+            ok = mbar_wait(bar(kFQEmpty + x), (qn[x] & 1) ^ 1, abort_flag, a.status);
+            if (!ok) continue;
+            mbar_arrive_expect_tx(bar(kFQFull + x), kFTile);
+            const uint32_t dq = s_base + kFSQ + x * kFTile;
+            tma_load_3d(dq, &tm_q, bar(kFQFull + x), 0, w.g * R, w.q0 + x * QPI);
+            tma_load_3d(dq + 16384, &tm_q, bar(kFQFull + x), 64, w.g * R, w.q0 + x * QPI);
+            ++qn[x];
+          }
         }
       }
       // copies still in flight land before the CTA may exit
