@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   const uint32_t tm = *tmem_holder;
   const int n_work = *a.n_items_k * a.G;
   KvItem w;
+  grid_dep_launch();   // dense_dq_kernel may follow wherever a CTA of this one ends
 
   if (warp < 4) {
     regs_dec<kBRegsRest>();
@@ -454,10 +455,9 @@ struct QItem {
   int g, q0, n, hi0, key0, m, n_kt;   // first packed query row, queries of the tile, last key of the first
 };
 template <int R>
-__device__ __forceinline__ bool q_item(const DenseArgs &a, int r, int n_work, QItem &w) {
+__device__ __forceinline__ bool q_item(const DenseArgs &a, int u, int n_work, QItem &w) {
   constexpr int QPI = 128 / R;
-  const int u = round_item(r, n_work);
-  if (u < 0) return false;
+  if (u >= n_work) return false;
   const int2 it = a.items[u / a.G];
   const int4 s = a.seqs[it.x];
   w.g = u % a.G;
@@ -473,12 +473,20 @@ __device__ __forceinline__ bool q_item(const DenseArgs &a, int r, int n_work, QI
 
 constexpr int kGQFull = 0, kGQEmpty = 1, kGKFull = 2, kGKEmpty = 5, kGVFull = 8, kGVEmpty = 10, kGSFull = 12,
               kGDpFull = 14, kGZFull = 15, kGAccFull = 16, kGAccEmpty = 17, kGReq = 18, kGClean = 19, kGDrain = 20,
-              kGNumBars = 21;
-constexpr int kGMisc = kGNumBars * 8;
+              kGItFull = 21, kGItEmpty = 23, kGNumBars = 25;
+constexpr int kGMisc = kGNumBars * 8;                // tmem holder, abort flag, two item numbers
 constexpr uint32_t kGTmS = 0, kGTmDP = 256, kGTmDQ = 384;   // S: two buffers of 128 columns
 
 // S of key tile j+1 runs under the softmax of tile j; dP of tile j+1 and
 // dQ += dZ K of tile j under the exponentials of tile j+1.
+//
+// This kernel needs nothing that dense_dkv_kernel makes, so it is launched as
+// its programmatic dependent: its CTAs take over an SM as soon as one of the
+// other's has ended there.  They start at different times, hence items are
+// handed out by a counter (by the producer, through a mailbox of two), which
+// evens out dk's and dv's long items: 7.3K tokens in seven documents 180 ->
+// 166 us for the whole backward.  Before it ends it waits for the other
+// kernel, so that what follows in the stream finds both done.
 template <int R>
 __global__ void __launch_bounds__(kBThreads, 1)
     dense_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -495,9 +503,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(ctl + kGMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(ctl + kGMisc + 4);
+  volatile int *s_item = reinterpret_cast<volatile int *>(ctl + kGMisc + 8);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < kGNumBars; ++i) mbar_init(bar(i), (i == kGZFull || i == kGAccEmpty) ? 256 : 1);
+    for (int i = 0; i < kGNumBars; ++i) mbar_init(bar(i), (i == kGZFull || i == kGAccEmpty) ? 256 : (i == kGItEmpty || i == kGItEmpty + 1) ? 10 : 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -511,6 +520,16 @@ __global__ void __launch_bounds__(kBThreads, 1)
   const uint32_t tm = *tmem_holder;
   const int n_work = *a.n_items * a.G;
   QItem w;
+  // The n-th item of this CTA, for its ten readers (one lane of the issuer,
+  // the cleaner and eight softmax warps): `all` of the warp's lanes call.
+  auto next_item = [&](uint32_t n, bool all) {
+    const uint32_t x = n & 1;
+    bool ok = mbar_wait(bar(kGItFull + x), (n >> 1) & 1, abort_flag, a.status);
+    const int it = s_item[x];
+    if (all) ok = __all_sync(0xffffffffu, ok);
+    if (ok && (!all || lane == 0)) mbar_arrive(bar(kGItEmpty + x));
+    return ok ? it : 0x7fffffff;
+  };
 
   if (warp < 4) {
     regs_dec<kBRegsRest>();
@@ -523,7 +542,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
       uint32_t it = 0, seq = 0, nk = 0;              // items; tiles of V and of K
       RingPos k, v;
       bool ok = true;
-      for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+      for (uint32_t n = 0; ok; ++n) {
+        ok = mbar_wait(bar(kGItEmpty + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag, a.status);
+        if (!ok) break;
+        const int item = atomicAdd(a.next_q, 1);
+        s_item[n & 1] = item;
+        mbar_arrive(bar(kGItFull + (n & 1)));
+        if (!q_item<R>(a, item, n_work, w)) break;
         if (w.n_kt == 0) continue;
         for (int j = 0; j < w.n_kt && ok; ++j, ++seq) {
           ok = mbar_wait(bar(kGKEmpty + k.s), k.ph ^ 1, abort_flag, a.status);
@@ -561,7 +586,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       uint32_t it = 0, seq = 0, cn = 0;
       RingPos k, v;
       bool ok = true;
-      for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+      for (uint32_t n = 0; ok && q_item<R>(a, next_item(n, false), n_work, w); ++n) {
         if (w.n_kt == 0) continue;
         ok = mbar_wait(bar(kGQFull), it & 1, abort_flag, a.status) &&
              mbar_wait(bar(kGKFull + k.s), k.ph, abort_flag, a.status);
@@ -616,7 +641,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       // score products that read it are issued or done.
       uint32_t seq = 0, cn = 0;
       bool ok = true;
-      for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+      for (uint32_t n = 0; ok && q_item<R>(a, next_item(n, true), n_work, w); ++n) {
         seq += w.n_kt;
         const int rem = w.m - (w.n_kt - 1) * 128;
         if (w.n_kt == 0 || rem >= 128) continue;
@@ -641,7 +666,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const float2 sc2 = f2_dup(a.scale_log2);
     uint32_t seq = 0, it = 0;
     bool ok = true;
-    for (int r = 0; ok && q_item<R>(a, r, n_work, w); ++r) {
+    for (uint32_t n = 0; ok && q_item<R>(a, next_item(n, true), n_work, w); ++n) {
       const bool valid = qi < w.n;
       const size_t qrow = size_t(w.q0 + qi) * a.H + w.g * R + hh;
       uint16_t *dq = a.dq + qrow * kHeadDim + hc * 64;
@@ -710,6 +735,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     tc_fence_after();
     tmem_dealloc(tm, 512);
   }
+  grid_dep_wait();
 }
 
 template <int R>
@@ -722,9 +748,19 @@ cudaError_t launch_bwd_r(const CUtensorMap &tq, const CUtensorMap &tdo, const CU
   const long long wk = (long long)a.max_items_k * a.G, wq = (long long)a.max_items * a.G;
   if (a.nk > 0)
     dense_dkv_kernel<R><<<unsigned(wk < num_sms ? wk : num_sms), kBThreads, kBSmem, st>>>(tq, tdo, tk, tv, a);
-  if (a.nq > 0)
-    dense_dq_kernel<R><<<unsigned(wq < num_sms ? wq : num_sms), kBThreads, kBSmem, st>>>(tq, tdo, tk, tv, a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.nq == 0) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(wq < num_sms ? wq : num_sms));
+  cfg.blockDim = dim3(kBThreads);
+  cfg.dynamicSmemBytes = kBSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.nk > 0 ? 1 : 0;   // without keys it follows the plan, which it needs
+  return cudaLaunchKernelEx(&cfg, dense_dq_kernel<R>, tq, tdo, tk, tv, a);
 }
 
 }  // namespace

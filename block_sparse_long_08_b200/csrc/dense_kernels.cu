@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(1024) dense_plan_kernel(const DenseArgs a, int
     base += total;
   }
   if (tid == 0) *(keys ? a.n_items_k : a.n_items) = base;
+  if (tid == 0 && keys) *a.next_q = 0;
   __syncthreads();
   __threadfence_block();
   // item x: its sequence (the last b with prefix[b] <= x) and place in it

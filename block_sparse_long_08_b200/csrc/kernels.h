@@ -265,6 +265,7 @@ struct DenseArgs {
   int2 *items_k;
   int *n_items_k;
   int max_items_k;
+  int *next_q;                 // counter that hands out dq's items (zeroed by the plan)
   float2 *stat;
   uint16_t *out;               // [nq,H,d] (read by the backward)
   float *lse;                  // [nq,H] or null

@@ -669,7 +669,7 @@ DenseWs dense_ws(const msa_params *p, bool backward) {
   w.items = o; o = align_up(o + sizeof(int2) * size_t(msa::dense_max_items(p->L, per, p->B)));
   w.count_k = w.prefix_k = w.items_k = w.stat = 0;
   if (backward) {
-    w.count_k = o; o = align_up(o + 4);
+    w.count_k = o; o = align_up(o + 8);   // and dq's counter
     w.prefix_k = o; o = align_up(o + 4 * (size_t(p->B) + 1));
     w.items_k = o; o = align_up(o + sizeof(int2) * size_t(msa::dense_max_items(p->L, 128, p->B)));
     w.stat = o; o = align_up(o + sizeof(float2) * size_t(p->L) * p->H);
@@ -772,9 +772,11 @@ int dense_args(const msa_params *p, int nq, int nk, const msa_bf16 *q, const msa
   a->max_items = msa::dense_max_items(nq, backward ? 128 / r : msa::dense_item_queries(r), p->B);
   a->fused = 0;
   a->prefix_k = nullptr; a->items_k = nullptr; a->n_items_k = nullptr; a->stat = nullptr;
+  a->next_q = nullptr;
   a->max_items_k = 0;
   if (backward) {
     a->n_items_k = reinterpret_cast<int *>(wsb + w.count_k);
+    a->next_q = a->n_items_k + 1;
     a->prefix_k = reinterpret_cast<int *>(wsb + w.prefix_k);
     a->items_k = reinterpret_cast<int2 *>(wsb + w.items_k);
     a->stat = reinterpret_cast<float2 *>(wsb + w.stat);
