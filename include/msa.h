@@ -413,8 +413,12 @@ int msa_nsa_forward(const msa_params *p, int32_t window, const msa_bf16 *q, cons
  *   lse[h] = ln sum_s exp(scale q[h].k[s,g]),  g = h/(H/G),
  *   s over the visible keys; a row that sees no key has out 0 and lse -inf.
  * Of params these calls use B, L, H, G, d and scale (d == 128, H/G in
- * {1,2,4,8,16}, B <= 2^20, L <= 2^26); d_idx, block, top_k and chunk are
- * ignored, and neither G <= 8 nor B*L <= 2^26 is asked for.
+ * {1,2,4,8,16}, H <= 1024, B <= 2^20, L <= 2^26); d_idx, block, top_k and
+ * chunk are ignored, and neither G <= 8 nor B*L <= 2^26 is asked for.
+ * Lengths, starts and page tables are device arrays that are read when the
+ * kernels run, so a captured call serves other lengths when it is replayed.
+ * Calls whose work may overlap (two streams, two graphs) need a workspace
+ * each.
  *
  * A paged cache.  Token t of sequence b lives in row t % page_size of page
  * page_table[b][t / page_size], one table for keys and values. */
