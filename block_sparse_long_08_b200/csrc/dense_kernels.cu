@@ -23,7 +23,7 @@
 // bf16).  Tried and slower: a quarter to half of the exponentials as
 // polynomials on the FMA pipe (1.98 ms at a quarter: an FMA pair takes two
 // issue slots), P handed over in halves (1.81 ms against 1.70 on one GPU: the
-// issuer then waits inside a tile), two softmax warpgroups per tile, an issuer per tile (the
+// issuer then waits inside a tile), two softmax warpgroups per tile, an issuer per tile (2.26 ms: the
 // products of both then finish late), S held back to interleave it with the
 // other tile's O (the tiles fall into step: 3.2 ms).
 //

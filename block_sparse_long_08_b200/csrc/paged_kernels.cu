@@ -411,57 +411,64 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
     ld.b = s_start[0]; ld.t = s_start[1];
     ld.len = pd_len(a, ld.b);
     PdCur cu = ld;
-    long long u_ld = u0;
+    // (no call has 2^31 tiles to a CTA)
+    const int n_u = int(u1 - u0);
+    int u_ld = 0;
+    const int32_t *tab = a.c.table + size_t(ld.b) * a.c.max_pages;
     auto page_of = [&](const PdCur &x) {
       const int key = x.t * kPdTile + warp * 16;
-      return key < x.len ? a.c.table[size_t(x.b) * a.c.max_pages + (key >> a.c.page_log2)] : 0;
+      return key < x.len ? tab[key >> a.c.page_log2] : 0;
     };
     int pg = page_of(ld);
+    // this lane's granule: row r0 (then every ROWS-th) of a step, granule gr
+    constexpr int GR = FP8 ? 8 : 16, ROWS = 32 / GR, EB = FP8 ? 1 : 2;
+    const int r0 = lane / GR, gr = lane % GR;
+    const uint32_t rowb = uint32_t(a.G) * (kHeadDim * EB);          // bytes between tokens
+    const uint8_t *k0p = static_cast<const uint8_t *>(a.c.k) + size_t(g) * (kHeadDim * EB) + gr * 16;
+    const uint8_t *v0p = static_cast<const uint8_t *>(a.c.v) + size_t(g) * (kHeadDim * EB) + gr * 16;
+    const float *s0p = FP8 ? (lane < 16 ? a.c.k_scale : a.c.v_scale) + g : nullptr;
     // copies of this warp's 16 keys of the next tile into ring stage st
     auto issue = [&](int st) {
-      if (u_ld < u1) {
+      if (u_ld < n_u) {
         const int key = ld.t * kPdTile + warp * 16;
         int vis = min(16, max(0, ld.len - key));
         if (vis > 0 && (pg < 0 || pg >= a.c.num_pages)) {
           vis = 0;
           if (lane == 0) atomicCAS(a.status, 0, kStatusBadInput);
         }
-        // (nothing is read where vis is 0: the row index stays inside the pool)
-        const size_t row = vis > 0 ? ((size_t(pg) << a.c.page_log2) + (key & pmask)) * a.G + g : 0;
+        // (nothing is read where vis is 0: the token stays inside the pool)
+        const unsigned long long tok = vis > 0 ? ((unsigned long long)pg << a.c.page_log2) + (key & pmask) : 0;
         const uint32_t dst = sm + st * C::STAGE;
-        // rows behind the visible ones are filled with zeros, not read
-        constexpr int GR = FP8 ? 8 : 16, ROWS = 32 / GR, EB = FP8 ? 1 : 2;
-        const int r0 = lane / GR, gr = lane % GR;
-        const size_t off0 = (row + size_t(r0 < vis ? r0 : 0) * a.G) * (kHeadDim * EB) + gr * 16;
-        const uint8_t *kp = static_cast<const uint8_t *>(a.c.k) + off0;
-        const uint8_t *vp = static_cast<const uint8_t *>(a.c.v) + off0;
-        const uint32_t stepb = uint32_t(a.G) * (ROWS * kHeadDim * EB);
         if (vis == 16) {
+          const unsigned long long off = (tok + r0) * rowb;
+          const uint8_t *kp = k0p + off, *vp = v0p + off;
 #pragma unroll
-          for (int i = 0; i < 16 / ROWS; ++i) {
+          for (int i = 0; i < 16 / ROWS; ++i, kp += ROWS * rowb, vp += ROWS * rowb) {
             const uint32_t d = swz<FP8>(r0 + ROWS * i, gr);
-            cpa16(dst + d, kp + i * size_t(stepb), 16u);
-            cpa16(dst + C::KB + d, vp + i * size_t(stepb), 16u);
+            cpa16(dst + d, kp, 16u);
+            cpa16(dst + C::KB + d, vp, 16u);
           }
+          if (FP8) cpa4(dst + 2 * C::KB + lane * 4, s0p + (tok + (lane & 15)) * a.G, 4u);
         } else {
+          // rows behind the visible ones are filled with zeros, not read
 #pragma unroll 1
           for (int i = 0; i < 16 / ROWS; ++i) {
             const int r = r0 + ROWS * i;
             const uint32_t d = swz<FP8>(r, gr), n = r < vis ? 16u : 0u;
-            const size_t o = r < vis ? i * size_t(stepb) : 0;
-            cpa16(dst + d, kp + o, n);
-            cpa16(dst + C::KB + d, vp + o, n);
+            const unsigned long long off = (tok + (r < vis ? r : 0)) * rowb;
+            cpa16(dst + d, k0p + off, n);
+            cpa16(dst + C::KB + d, v0p + off, n);
+          }
+          if (FP8) {
+            const int r = lane & 15;
+            cpa4(dst + 2 * C::KB + lane * 4, s0p + (tok + (r < vis ? r : 0)) * a.G, r < vis ? 4u : 0u);
           }
         }
-        if (FP8) {
-          const int r = lane & 15;
-          const float *sp = (lane < 16 ? a.c.k_scale : a.c.v_scale) + row + (r < vis ? size_t(r) * a.G : 0);
-          cpa4(dst + 2 * C::KB + lane * 4, sp, r < vis ? 4u : 0u);
-        }
         if (lane == 0) s_vis[st] = vis;
-        ++u_ld;
-        if (u_ld < u1) {
+        if (++u_ld < n_u) {
+          const int b = ld.b;
           ld.next(a);
+          if (ld.b != b) tab = a.c.table + size_t(ld.b) * a.c.max_pages;
           pg = page_of(ld);   // used at the next issue
         }
       }
@@ -482,9 +489,9 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
     uint32_t qf[8][4];
     bool fresh = true;                              // a new pair: its queries are to be loaded
     bool head = cu.t > 0;                           // the pair began in an earlier run
-    long long pair_left = 0;
+    int pair_left = 0;
     int st = 0;
-    for (long long u = u0; u < u1; ++u) {
+    for (int u = 0; u < n_u; ++u) {
       if (fresh) {
         fresh = false;
         pair_left = cu.tiles() - cu.t;
@@ -513,9 +520,9 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 u0 = *reinterpret_cast<const uint4 *>(ks + swz<true>(g4, c + 4 * h));
-          const uint4 u1 = *reinterpret_cast<const uint4 *>(ks + swz<true>(g4 + 8, c + 4 * h));
-          const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+          const uint4 r0 = *reinterpret_cast<const uint4 *>(ks + swz<true>(g4, c + 4 * h));
+          const uint4 r1 = *reinterpret_cast<const uint4 *>(ks + swz<true>(g4 + 8, c + 4 * h));
+          const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const uint32_t ka[4] = {f16x2_of_e4m3x2(w0[x]), f16x2_of_e4m3x2(w1[x]), f16x2_of_e4m3x2(w0[x] >> 16),
@@ -542,12 +549,12 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         }
         // two references as below: m for the sums, mw for the weights that
         // multiply V's codes (P |scale|, f16); both in log2 units here
-        const bool u0 = m0 == -INFINITY || x0 - m0 > 8.f, u1 = m1 == -INFINITY || x1 - m1 > 8.f;
+        const bool up0 = m0 == -INFINITY || x0 - m0 > 8.f, up1 = m1 == -INFINITY || x1 - m1 > 8.f;
         const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > 8.f);
         const bool wu1 = y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > 8.f);
-        if (__any_sync(0xffffffffu, u0 || u1 || wu0 || wu1)) {
-          if (u0) { l0 *= m0 == -INFINITY ? 0.f : exp2_fast(m0 - x0); m0 = x0; }
-          if (u1) { l1 *= m1 == -INFINITY ? 0.f : exp2_fast(m1 - x1); m1 = x1; }
+        if (__any_sync(0xffffffffu, up0 || up1 || wu0 || wu1)) {
+          if (up0) { l0 *= m0 == -INFINITY ? 0.f : exp2_fast(m0 - x0); m0 = x0; }
+          if (up1) { l1 *= m1 == -INFINITY ? 0.f : exp2_fast(m1 - x1); m1 = x1; }
           const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - y0)) : 1.f;
           const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - y1)) : 1.f;
           if (wu0) mw0 = y0;
@@ -752,7 +759,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
 
       // ---- the pair's end, or the run's: join the four warps
       const bool done = --pair_left == 0;
-      if (done || u + 1 == u1) {
+      if (done || u + 1 == n_u) {
         const int h0 = C::KM ? 2 * c : g4, h1 = C::KM ? 2 * c + 1 : g4 + 8;   // this lane's heads
 #pragma unroll
         for (int i = C::KM ? 4 : 1; i < (C::KM ? 32 : 4); i <<= 1) {
@@ -775,9 +782,9 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
           M1 = fmaxf(M1, s_m[w * 16 + h1]);
         }
         // O's unit, 2^(scale m) (8-bit: 2^mw), to 2^(scale M)
-        const float u0 = FP8 ? mw0 : m0 * a.scale_log2, u1 = FP8 ? mw1 : m1 * a.scale_log2;
-        const float f0 = u0 == -INFINITY ? 0.f : exp2_fast(u0 - M0 * a.scale_log2);
-        const float f1 = u1 == -INFINITY ? 0.f : exp2_fast(u1 - M1 * a.scale_log2);
+        const float unit0 = FP8 ? mw0 : m0 * a.scale_log2, unit1 = FP8 ? mw1 : m1 * a.scale_log2;
+        const float f0 = unit0 == -INFINITY ? 0.f : exp2_fast(unit0 - M0 * a.scale_log2);
+        const float f1 = unit1 == -INFINITY ? 0.f : exp2_fast(unit1 - M1 * a.scale_log2);
         // warp by warp, so that the sum's order is always the same
         for (int w = 0; w < 4; ++w) {
           if (C::KM && w == warp) {
@@ -835,7 +842,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         }
         if (!CL && !done && !head) {
           // the pair ends with tile u + pair_left: parts up to the group whose run holds that
-          const long long e = u + 1 + pair_left;
+          const long long e = u0 + u + 1 + pair_left;
           meta = make_int4(cu.b, g, int((e * n_grp + T - 1) / T - 1) - grp + 1, 0);
         }
         __syncthreads();   // s_o, s_m and s_l are free again
@@ -848,7 +855,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         fresh = true;
         head = false;
       }
-      if (u + 1 < u1) cu.next(a);
+      if (u + 1 < n_u) cu.next(a);
     }
     cpa_wait<0>();
   }
