@@ -175,7 +175,12 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
       const float scale = m > 0.f ? m / 448.f : 1.f;
-      const float inv = 1.f / scale;
+      float inv = 1.f / scale;
+      if (scale < 0x1p-120f) {   // 1 / scale may overflow: divide by it
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], scale);
+        inv = 1.f;
+      }
       uint8_t *dst = static_cast<uint8_t *>(is_v ? a.c.v : a.c.k) + crow * kHeadDim;
       *reinterpret_cast<uint2 *>(dst + e0) = codes8(x, inv);
       *reinterpret_cast<uint2 *>(dst + e1) = codes8(x + 8, inv);
@@ -224,7 +229,7 @@ struct PdCfg {
   static constexpr bool KM = FP8 && R <= 8;
   static constexpr int NST = 3;
   static constexpr int CTAS = KM ? 4 : FP8 ? 3 : 2;   // per SM (8-bit, 96 x <= 16K tokens: 4 321 us, 3 326 us)
-  static constexpr int SCR = FP8 && !KM ? 4096 : 0;   // a step's V rows as bf16
+  static constexpr int SCR = FP8 && !KM ? 4096 : 0;   // a step's V rows as f16
   static constexpr int WARP = NST * STAGE + SCR;
   static constexpr int OFF_O = 4 * WARP;       // [R][128] fp32
   static constexpr int OFF_ML = OFF_O + R * kHeadDim * 4;   // [4][16] maxima, [4][16] sums

@@ -407,3 +407,27 @@ def test_decode_fp8_scales_of_any_size(scales):
         c["vs"] = torch.where(c["own"][..., None].to(DEV), torch.zeros_like(c["vs"]), float("nan"))
         out, _ = decode(c, q, lens)
         assert (out == 0).all()
+
+
+def test_append_fp8_rows_of_tiny_and_large_values():
+    """Rows whose scale is subnormal, or whose values end at the type's top."""
+    G, page = 4, 16
+    k = torch.zeros(1, G, 128, dtype=BF16)
+    k[0, 0, :64] = 1e-40                 # subnormal values, zeros beside them
+    k[0, 1] = (torch.linspace(-1, 1, 128) * 3.3e38).to(BF16)
+    k[0, 2] = torch.linspace(-1e-36, 1e-36, 128).to(BF16)
+    k[0, 3, 5] = 2.0 ** -133             # the smallest subnormal
+    assert torch.isfinite(k).all()
+    k = k.to(DEV)
+    kp, vp = (torch.zeros(2, page, G, 128, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros(2, page, G, device=DEV) for _ in range(2))
+    table = torch.tensor([[1]], dtype=torch.int32, device=DEV)
+    M.msa_paged_append(k, k, kp, vp, table, torch.tensor([4], dtype=torch.int32, device=DEV), k_scale=ks, v_scale=vs)
+    codes = kp[1, 3].cpu()
+    got = codes.view(torch.float8_e4m3fn).float()
+    assert torch.isfinite(got).all()
+    want = f64(k[0])
+    rel = got.double().numpy() / 448 * np.abs(want).max(-1, keepdims=True)
+    # half a step of a code (2^-4 of a normal one), and the largest is met
+    assert (np.abs(rel - want) <= np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -9 * np.abs(want).max(-1, keepdims=True))).all()
+    assert (got.abs().amax(-1) == 448).all()
