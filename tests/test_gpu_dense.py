@@ -345,3 +345,15 @@ def test_short_sequences_back_to_back_repeat(n, G, R):
         b = run(x, cq, ck)
         gb = M.msa_dense_attn_varlen_backward(x["q"], x["k"], x["v"], *b, x["dout"], i32(cq), i32(ck))
         assert all(torch.equal(s, t) for s, t in zip(a + tuple(ga), b + tuple(gb)))
+
+
+def test_bad_starts_of_a_large_batch_are_refused_whole():
+    """The listed plan's refusal in the forward (more sequences than a call
+    plans for itself)."""
+    lens = [20] * 50
+    x, cq, ck = packed(lens, lens, 1, 2)
+    cq[30] = cq[29] - 1
+    ws = M.new_dense_workspace(M.MSA_OP_DENSE_VARLEN, x["q"], x["k"], 50)
+    out, lse = run(x, cq, ck, ws=ws)
+    assert M.msa_read_status(ws) == M.MSA_ERR_DEVICE_INPUT
+    assert (out == 7).all() and (lse == 7).all()
