@@ -40,7 +40,7 @@ constexpr int kBTile = 32768;                       // 128 rows x 256 B
 // statistics lie in 3 KB of static memory before it, so that the tiles start
 // on a 1024-byte boundary without slack.
 constexpr int kBSKeep = 0, kBSLong = 2 * kBTile, kBSShort = 5 * kBTile, kBSmem = 7 * kBTile;
-constexpr int kBCtl = 3072;
+constexpr int kBCtl = 3 * 1024;
 static_assert(kBSmem + kBCtl <= 232448, "shared memory budget");
 // A place in a ring of n stages and the phase of its use.
 struct RingPos {

@@ -18,14 +18,18 @@
 // The two tiles take turns: one's softmax runs under the other's products.
 // A tile's chain (softmax 1700 cycles, then O += P V and the next S, 1400
 // with the hand-overs) sets the pace: S and P share TMEM columns (2 x 128 for
-// S and 2 x 128 for O are all there is), so S cannot run ahead.  Measured:
-// 32K tokens, 8 heads on 1 KV head 1.94 ms (1136 TFLOP/s, 0.69 of burst
-// bf16).  Tried and slower: a quarter to half of the exponentials as
-// polynomials on the FMA pipe (1.98 ms at a quarter: an FMA pair takes two
-// issue slots), P handed over in halves (1.81 ms against 1.70 on one GPU: the
-// issuer then waits inside a tile), two softmax warpgroups per tile, an issuer per tile (2.26 ms: the
-// products of both then finish late), S held back to interleave it with the
-// other tile's O (the tiles fall into step: 3.2 ms).
+// S and 2 x 128 for O are all there is), so S cannot run ahead.
+// Measured: 32K tokens, 8 heads on 1 KV head, 1.70 ms from idle (1294
+// TFLOP/s, 0.78 of burst bf16) and 1.91 ms in a long power-capped run.
+// Tried and slower, each against its own start:
+//   - a quarter of the exponentials as polynomials on the FMA pipe, 1.98 ms
+//     against 1.94 (a packed FMA takes two issue slots);
+//   - P handed over in halves, 1.81 against 1.70 (the issuer waits inside a
+//     tile while the other tile's product could go);
+//   - two softmax warpgroups per tile, 2.61 against 2.12;
+//   - an issuer per tile, 2.26 against 1.71 (both chains then finish late);
+//   - S held back to interleave it with the other tile's O, 3.22 against 2.12
+//     (the tiles fall into step).
 //
 // Roles (one persistent CTA per SM, four warpgroups):
 //   warp 0     TMA producer: the tiles' Q, then K and V of each key tile, into
@@ -214,7 +218,7 @@ constexpr int kFTile = 32768;                    // 128 rows x 256 B
 constexpr int kFNkv = 5;                         // K/V ring depth
 constexpr int kFSQ = 0;                          // two Q tiles
 constexpr int kFSKV = 2 * kFTile;
-constexpr int kFCtl = kFSKV + kFNkv * kFTile;
+constexpr int kFSmem = kFSKV + kFNkv * kFTile;
 // barriers
 constexpr int kFQFull = 0, kFQEmpty = 2, kFKvFull = 4, kFKvEmpty = 4 + kFNkv,
               kFSFull = 4 + 2 * kFNkv, kFPFull = kFSFull + 2, kFOFull = kFPFull + 2,
@@ -224,9 +228,9 @@ constexpr int kFCtlMisc = kFNumBars * 8;         // tmem holder, abort flag
 constexpr int kFCtlX = (kFCtlMisc + 8 + 15) & ~15;   // [2][128] row sums, [2][128] reference maxima
 constexpr int kFCtlSmall = kFCtlX + 4 * 128 * 4;      // FSmall
 constexpr int kFBytes = kFCtlSmall + 32 * 16 + 33 * 4;
-static_assert(kFBytes <= 3072, "control block");
-constexpr int kFSmem = kFCtl;
-static_assert(kFSmem + 3072 <= 232448, "shared memory budget");
+constexpr int kFStatic = 3 * 1024;   // static shared memory of the control block
+static_assert(kFBytes <= kFStatic, "control block");
+static_assert(kFSmem + kFStatic <= 232448, "shared memory budget");
 // TMEM columns: S (then P) of tile A and B, O of A and B
 constexpr uint32_t kFTmS = 0, kFTmO = 256;
 
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   // the tiles fill the dynamic memory; 3 KB of static memory before them, so
   // that they start on a 1024-byte boundary without slack
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(1024) uint8_t ctl[3072];
+  __shared__ __align__(1024) uint8_t ctl[kFStatic];
   const uint32_t s_base = smem_u32(smem);
   if (s_base & 1023) {   // the tiles' swizzle needs it
     if (threadIdx.x == 0) atomicCAS(a.status, 0, kStatusTimeout);

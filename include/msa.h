@@ -478,8 +478,9 @@ int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, 
  * outside [0, p->L] sets MSA_ERR_DEVICE_INPUT (out 0, lse -inf); the keys of
  * a page whose id lies outside [0, num_pages) are left out and set it too.
  * The cache's tokens are shared out over the SMs whatever the lengths, the
- * parts of one sequence joined by a second launch; the split depends on
- * the lengths alone, so results repeat bit for bit.
+ * parts of one sequence joined by a second launch (short calls: within one);
+ * the split depends on the lengths and p alone, so results repeat bit for
+ * bit.
  * An 8-bit cache's scores run in f16 (|q| < 65504); each value's scale is
  * folded into its softmax weight before the weight is rounded to f16.
  * ws >= msa_workspace_bytes(p, MSA_OP_PAGED_DECODE). */
