@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         on ^= 1;
         const float l = s_l[x * 128 + row], mr = s_m[x * 128 + row];
         mbar_arrive(bar(kFLEmpty + x));
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // (a NaN stays one)
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(bar(kFOEmpty + x));
-        if (valid && a.lse) a.lse[orow] = l > 0.f ? mr * a.scale + logf(l) : -INFINITY;
+        if (valid && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : mr * a.scale + logf(l);
       }
     }
   }

@@ -838,8 +838,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
             if (tid == 0) s_part[r] = make_float2(M, L);
           } else if (whole) {
             const size_t orow = size_t(cu.b) * a.H + g * R + r;
-            reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + tid] = __float2bfloat16(L > 0.f ? x / L : 0.f);
-            if (tid == 0 && a.lse) a.lse[orow] = L > 0.f ? M * a.scale + logf(L) : -INFINITY;
+            reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + tid] = __float2bfloat16(L == 0.f ? 0.f : x / L);
+            if (tid == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : M * a.scale + logf(L);
           } else {
             part[r * kPdRow + tid] = x;
             if (tid == 0) { part[r * kPdRow + kHeadDim] = M; part[r * kPdRow + kHeadDim + 1] = L; }
@@ -887,8 +887,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         O = m[p] == -INFINITY ? O : fmaf(f, x[p], O);   // (a CTA without tiles left x unwritten)
       }
       const size_t orow = size_t((cta >> 3) / a.G) * a.H + g * R + r;
-      reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + tid] = __float2bfloat16(L > 0.f ? O / L : 0.f);
-      if (tid == 0 && a.lse) a.lse[orow] = L > 0.f ? M * a.scale + logf(L) : -INFINITY;
+      reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + tid] = __float2bfloat16(L == 0.f ? 0.f : O / L);
+      if (tid == 0 && a.lse) a.lse[orow] = L == 0.f ? -INFINITY : M * a.scale + logf(L);
     }
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
     if ((cta & 7) == 0 && g == 0 && tid == 0) {
@@ -947,8 +947,8 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const PagedDecodeArgs a
   x = (s_x[0][d] + s_x[1][d]) + (s_x[2][d] + s_x[3][d]);
   l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
   const size_t orow = size_t(meta.x) * a.H + meta.y * R + r;
-  reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + d] = __float2bfloat16(l > 0.f ? x / l : 0.f);
-  if (d == 0 && a.lse) a.lse[orow] = l > 0.f ? M * a.scale + logf(l) : -INFINITY;
+  reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * kHeadDim + d] = __float2bfloat16(l == 0.f ? 0.f : x / l);
+  if (d == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : M * a.scale + logf(l);
 }
 
 template <int R, bool FP8>

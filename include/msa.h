@@ -474,7 +474,9 @@ int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, 
  *   seq_lens [B] int32 DEVICE: cached tokens of each sequence, in [0, p->L];
  *     0 (a padding sequence) gives out 0, lse -inf                       (in)
  *   out [B,H,d] bf16; lse [B,H] fp32 or NULL                            (out)
- * Cache rows at and behind seq_lens[b] may hold anything.  seq_lens[b]
+ * Cache rows at and behind seq_lens[b] may hold anything; a NaN in a query or
+ * an attended row makes that head's out (a key's: its lse too) NaN, and
+ * nothing else.  seq_lens[b]
  * outside [0, p->L] sets MSA_ERR_DEVICE_INPUT (out 0, lse -inf); the keys of
  * a page whose id lies outside [0, num_pages) are left out and set it too.
  * The cache's tokens are shared out over the SMs whatever the lengths, the
@@ -499,7 +501,8 @@ int msa_paged_attn_decode(const msa_params *p, const msa_paged_cache *c, const m
  * Rows at and behind cu_q[B] are left as they were.  cu_q or cu_k not
  * ascending inside [0, nq] or [0, nk] sets MSA_ERR_DEVICE_INPUT and nothing
  * is written.  A sequence's own keys and values are finite; rows of other
- * sequences and rows behind the last one may hold anything.
+ * sequences and rows behind the last one may hold anything.  A NaN in a query
+ * makes that row's out and lse NaN, and nothing else.
  * ws >= msa_workspace_bytes(p, MSA_OP_DENSE_VARLEN). */
 int msa_dense_attn_varlen(const msa_params *p, int nq, int nk, const msa_bf16 *q,
                           const msa_bf16 *k, const msa_bf16 *v, const int32_t *cu_q,

@@ -357,3 +357,17 @@ def test_bad_starts_of_a_large_batch_are_refused_whole():
     out, lse = run(x, cq, ck, ws=ws)
     assert M.msa_read_status(ws) == M.MSA_ERR_DEVICE_INPUT
     assert (out == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("R", [1, 4, 16])
+def test_nan_in_a_query_stays_in_its_row(R):
+    lens = [3, 300, 40]
+    x, cq, ck = packed(lens, lens, 2, R, seed=R)
+    out, lse = run(x, cq, ck)
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    for i, h in ((1, 0), (150, 2 * R - 1), (302, R)):
+        x["q"][i, h, 7] = float("nan")
+        hit[i, h] = True
+    o, ls = run(x, cq, ck)
+    assert torch.isnan(o[hit]).all() and torch.isnan(ls[hit]).all()
+    assert torch.equal(o[~hit], out[~hit]) and torch.equal(ls[~hit], lse[~hit])

@@ -431,3 +431,27 @@ def test_append_fp8_rows_of_tiny_and_large_values():
     # half a step of a code (2^-4 of a normal one), and the largest is met
     assert (np.abs(rel - want) <= np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -9 * np.abs(want).max(-1, keepdims=True))).all()
     assert (got.abs().amax(-1) == 448).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G,R,lens", [(2, 4, [40, 900, 70]), (1, 16, [3, 5000]), (4, 8, [20000, 300, 9000] + [1] * 30)])
+def test_decode_nan_stays_with_its_head(G, R, lens, fp8):
+    """Token 17 of sequence 1 holds a NaN key (head 0) or value (the last
+    head): that head's results are NaN, all others keep their bits."""
+    c = make_cache(lens, G, 16, fp8, seed=G)
+    q = torch.randn(len(lens), G * R, 128, generator=torch.Generator().manual_seed(4)).to(BF16).to(DEV)
+    out, lse = decode(c, q, lens)
+    at = (int(c["table"][1, 1]), 1)
+    for x, g in (("k", 0), ("v", G - 1)):
+        bad = dict(c)
+        bad[x] = c[x].clone()
+        bad[x][at[0], at[1], g] = 0x7F if fp8 else float("nan")
+        o, ls = decode(bad, q, lens)
+        hit = torch.zeros(len(lens), G * R, dtype=torch.bool, device=DEV)
+        hit[1, g * R:(g + 1) * R] = True
+        assert torch.isnan(o[hit]).all() and torch.equal(o[~hit], out[~hit])
+        if x == "k":
+            assert torch.isnan(ls[hit]).all()
+        else:
+            assert torch.equal(ls[hit], lse[hit])
+        assert torch.equal(ls[~hit], lse[~hit])
