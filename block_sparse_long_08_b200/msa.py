@@ -776,10 +776,20 @@ def _dense_params(B, L, H, G, d, scale=0.0):
     return msa_params(B, L, H, G, d, 128, 128, 16, scale, 0)
 
 
-def _call_ws(ws, p, op, dev):
+def _new(make, stream):
+    """A tensor that the call allocates, on the stream it runs on: its memory
+    may hold other work's data on any other one, and is given to others there
+    as soon as the tensor is dropped."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _call_ws(ws, p, op, dev, stream):
     """(workspace, its address and size): allocated for the call when None."""
     if ws is None:
-        ws = torch.zeros(msa_workspace_bytes(p, op), dtype=_U8, device=dev)
+        ws = _new(lambda: torch.zeros(msa_workspace_bytes(p, op), dtype=_U8, device=dev), stream)
     return ws, _fits(ws, "ws", _U8, 0, dev), ws.numel()
 
 
@@ -845,7 +855,7 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
     if q is not None:
         H = q.shape[1]
         qa = _fits(q, "q", _BF16, N * H * d, dev)
-        q_out = torch.empty_like(q) if q_out is None else q_out
+        q_out = _new(lambda: torch.empty_like(q), stream) if q_out is None else q_out
         qo = _fits(q_out, "q_out", _BF16, N * H * d, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -855,7 +865,7 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
     fa = _fits(inv_freq, "inv_freq", _F32, rot_dim // 2, dev) if rot_dim else None
     ko = None if k_out is None else _fits(k_out, "k_out", _BF16, kv, dev)
     p = _dense_params(B, L, H, G, d)
-    ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_APPEND, dev)
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_APPEND, dev, stream)
     _launch(lib().msa_paged_append, dev, ctypes.byref(p), ctypes.byref(c), N, qa, k.data_ptr(), va, cu,
             la, fa, int(rot_dim), int(bool(interleaved)), qo, ko, wa, wn, _stream_on(stream, dev))
     return q_out
@@ -875,13 +885,13 @@ def msa_paged_attn_decode(q, k_pages, v_pages, page_table, seq_lens, *, k_scale=
     if Bt < B:
         raise ValueError(f"page_table rows: the call needs {B}, there are {Bt}")
     la = _fits(seq_lens, "seq_lens", _I32, B, dev)
-    out = torch.empty_like(q) if out is None else out
+    out = _new(lambda: torch.empty_like(q), stream) if out is None else out
     oa = _fits(out, "out", _BF16, B * H * d, dev)
     if lse is None and want_lse:
-        lse = torch.empty((B, H), dtype=_F32, device=dev)
+        lse = _new(lambda: torch.empty((B, H), dtype=_F32, device=dev), stream)
     ea = None if lse is None else _fits(lse, "lse", _F32, B * H, dev)
     p = _dense_params(B, L, H, G, d, scale)
-    ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_DECODE, dev)
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_PAGED_DECODE, dev, stream)
     _launch(lib().msa_paged_attn_decode, dev, ctypes.byref(p), ctypes.byref(c), q.data_ptr(), la, oa, ea,
             wa, wn, _stream_on(stream, dev))
     return (out, lse) if lse is not None else out
@@ -908,12 +918,12 @@ def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: 
     given).  Rows behind cu_q[B] are left as they were."""
     nq, nk, p, adr, cus, dev = _dense_inputs(q, k, v, cu_q, cu_k, scale)
     H = q.shape[1]
-    out = torch.empty_like(q) if out is None else out
+    out = _new(lambda: torch.empty_like(q), stream) if out is None else out
     oa = _fits(out, "out", _BF16, q.numel(), dev)
     if lse is None and want_lse:
-        lse = torch.empty((nq, H), dtype=_F32, device=dev)
+        lse = _new(lambda: torch.empty((nq, H), dtype=_F32, device=dev), stream)
     ea = None if lse is None else _fits(lse, "lse", _F32, nq * H, dev)
-    ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN, dev)
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN, dev, stream)
     _launch(lib().msa_dense_attn_varlen, dev, ctypes.byref(p), nq, nk, *adr, *cus, oa, ea, wa, wn,
             _stream_on(stream, dev))
     return (out, lse) if lse is not None else out
@@ -925,13 +935,13 @@ def msa_dense_attn_varlen_backward(q, k, v, out, lse, dout, cu_q, cu_k, *, scale
     [nq,H], dout [nq,H,d] -> (dq, dk, dv) bf16, shaped like q, k, v."""
     nq, nk, p, adr, cus, dev = _dense_inputs(q, k, v, cu_q, cu_k, scale)
     nkv = nk * k.shape[1] * k.shape[2]
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new(lambda: torch.empty_like(q), stream) if dq is None else dq
+    dk = _new(lambda: torch.empty_like(k), stream) if dk is None else dk
+    dv = _new(lambda: torch.empty_like(v), stream) if dv is None else dv
     oa, da, qa = (_fits(t, n, _BF16, q.numel(), dev) for n, t in (("out", out), ("dout", dout), ("dq", dq)))
     ka, va = (_fits(t, n, _BF16, nkv, dev) for n, t in (("dk", dk), ("dv", dv)))
     ea = _fits(lse, "lse", _F32, nq * q.shape[1], dev)
-    ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, dev)
+    ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, dev, stream)
     _launch(lib().msa_dense_attn_varlen_backward, dev, ctypes.byref(p), nq, nk, *adr, oa, ea, da, *cus,
             qa, ka, va, wa, wn, _stream_on(stream, dev))
     return dq, dk, dv

@@ -371,3 +371,35 @@ def test_nan_in_a_query_stays_in_its_row(R):
     o, ls = run(x, cq, ck)
     assert torch.isnan(o[hit]).all() and torch.isnan(ls[hit]).all()
     assert torch.equal(o[~hit], out[~hit]) and torch.equal(ls[~hit], lse[~hit])
+
+
+def test_what_a_call_allocates_belongs_to_the_given_stream():
+    """The stream is busy while the call is made, and other work of the current
+    one takes memory of the same sizes at once."""
+    lens = [600, 90, 1]
+    x, cq, ck = packed(lens, lens, 2, 4, seed=12)
+    out, lse = run(x, cq, ck)
+    grads = M.msa_dense_attn_varlen_backward(x["q"], x["k"], x["v"], out, lse, x["dout"], i32(cq), i32(ck))
+    nk = x["k"].shape[0]
+    table = torch.arange(64, dtype=torch.int32, device=DEV).reshape(1, 64)
+    kp, vp = (torch.zeros(64, 16, 2, 128, dtype=BF16, device=DEV) for _ in range(2))
+    n = i32([nk])
+    M.msa_paged_append(x["k"], x["v"], kp, vp, table, n, cu_new=i32([0, nk]))
+    one = M.msa_paged_attn_decode(x["q"][:1], kp, vp, table, n)
+    cqd, ckd = i32(cq), i32(ck)
+    s = torch.cuda.Stream()
+
+    def calls():
+        o, ls = M.msa_dense_attn_varlen(x["q"], x["k"], x["v"], cqd, ckd, want_lse=True, stream=s)
+        g = M.msa_dense_attn_varlen_backward(x["q"], x["k"], x["v"], out, lse, x["dout"], cqd, ckd, stream=s)
+        return (o, ls) + tuple(g) + (M.msa_paged_attn_decode(x["q"][:1], kp, vp, table, n, stream=s),)
+
+    calls()                                   # (freed memory of these sizes is there to be taken)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    got = calls()
+    junk = [torch.full((2 ** i,), 255, dtype=torch.uint8, device=DEV) for i in range(8, 22) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (out, lse) + tuple(grads) + (one,)))
+    assert all((j == 255).all() for j in junk)
