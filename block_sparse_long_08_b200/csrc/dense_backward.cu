@@ -374,23 +374,31 @@ __global__ void __launch_bounds__(kBThreads, 1)
         load64(tl + kVTmS + hc * 64, p);
         tc_fence_before();
         mbar_arrive(bar(kVSFree));
-        // rows that see this key: query qa + row / R >= key - rel, up to the last query
-        const int lo = (key - w.rel - qa) * R - hc * 64, hi = (w.n - qa) * R - hc * 64;
-        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
-        const float4 *nl = reinterpret_cast<const float4 *>(s_nl + st * 128 + hc * 64);
+        // rows that see this key: queries >= key - rel, up to the last one; in
+        // the queries of this warpgroup's half (64 / R of them, R rows each)
+        constexpr int QH = 64 / R;
+        const int lo = key - w.rel - qa - hc * QH, hi = w.n - qa - hc * QH;
+        const bool tail = hi < QH;
+        const bool masked = __any_sync(0xffffffffu, lo > 0 || tail);
+        if (masked && __all_sync(0xffffffffu, lo >= min(hi, QH))) {   // no row sees a key of this warp
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float4 x = nl[c];
-          const float2 z0 = f2_fma(make_float2(p[4 * c], p[4 * c + 1]), sc2, make_float2(x.x, x.y));
-          const float2 z1 = f2_fma(make_float2(p[4 * c + 2], p[4 * c + 3]), sc2, make_float2(x.z, x.w));
-          p[4 * c] = fast_exp2(z0.x);
-          p[4 * c + 1] = fast_exp2(z0.y);
-          p[4 * c + 2] = fast_exp2(z1.x);
-          p[4 * c + 3] = fast_exp2(z1.y);
-        }
-        if (masked) {
+          for (int c = 0; c < 64; ++c) p[c] = 0.f;
+        } else {
+          const float4 *nl = reinterpret_cast<const float4 *>(s_nl + st * 128 + hc * 64);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
+          for (int c = 0; c < 16; ++c) {
+            const float4 x = nl[c];
+            const float2 z0 = f2_fma(make_float2(p[4 * c], p[4 * c + 1]), sc2, make_float2(x.x, x.y));
+            const float2 z1 = f2_fma(make_float2(p[4 * c + 2], p[4 * c + 3]), sc2, make_float2(x.z, x.w));
+            p[4 * c] = fast_exp2(z0.x);
+            p[4 * c + 1] = fast_exp2(z0.y);
+            p[4 * c + 2] = fast_exp2(z1.x);
+            p[4 * c + 3] = fast_exp2(z1.y);
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) p[c] = (c / R >= lo && c / R < hi) ? p[c] : 0.f;
+          }
         }
         ok = mbar_wait(bar(kVDpFull), seq & 1, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -411,9 +419,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
           z[4 * c] = z0.x; z[4 * c + 1] = z0.y;
           z[4 * c + 2] = z1.x; z[4 * c + 3] = z1.y;
         }
-        if (masked) {
+        if (tail) {   // (dP of the rows behind the last query may be anything)
 #pragma unroll
-          for (int c = 0; c < 64; ++c) z[c] = (c >= lo && c < hi) ? z[c] : 0.f;
+          for (int c = 0; c < 64; ++c) z[c] = c / R < hi ? z[c] : 0.f;
         }
         store64(tl + kVTmDP + hc * 64 + 32, z);
         tc_fence_before();
