@@ -16,6 +16,19 @@
 // S and dP are computed in both kernels: 7 products where one kernel with
 // atomics on dq would need 5.  In return no gradient is summed by atomics (the
 // result repeats bit for bit) and nothing of dq's size is kept in fp32.
+// P and dZ are rounded to bf16 for their products (Q, K and dO are bf16, and
+// both operands of a UMMA have one type).  Every element's rounding is its own,
+// of the size of the results' last one: dq and dk are 2.5e-3 of their norm off
+// where a single rounding at the end gives 1.7e-3, dv 2.3e-3.  D comes from
+// out as bf16, as the caller holds it.
+// Measured: 8192 tokens, 32 heads on 8, 1.34 ms from idle (7 products of 128^3
+// per tile pair; 1026 TFLOP/s, 0.62 of burst bf16, over the 5 counted); 7.3K tokens in seven
+// documents, 16 heads on 4, 136-158 us.  A step of dkv takes 2680 cycles for
+// 2050 of products, one of dq 2020 for 1540: the softmax's chain (exponentials
+// 1030 of the MUFU unit, loads and stores of TMEM around them) bounds both.
+// Tried and not faster: exponentials as polynomials on the FMA pipe, K and V
+// (Q and dO) released before the last product, dq stored under the next item's
+// first products, halves of a dq tile skipped where no row sees them.
 // Roles in both kernels (one persistent CTA per SM, three warpgroups): warp 0
 // loads by TMA, warp 1 issues UMMAs, warps 2-3 help, warps 4-11 are the
 // softmax: two warpgroups, one TMEM lane per thread, 64 of the 128 columns

@@ -29,7 +29,14 @@
 //   - two softmax warpgroups per tile, 2.61 against 2.12;
 //   - an issuer per tile, 2.26 against 1.71 (both chains then finish late);
 //   - S held back to interleave it with the other tile's O, 3.22 against 2.12
-//     (the tiles fall into step).
+//     (the tiles fall into step);
+//   - S in two buffers of 64 keys, ahead of the products into O: 2.83 against
+//     1.65, with an issuer per tile 1.82 (a product of N = 64 takes the issuer
+//     as long as one of 128);
+//   - the next item's first S right behind each tile's last product, 1.82
+//     against 1.67.
+// P is rounded to bf16 for its product with V (both operands of a UMMA have one
+// type); the row's sum takes it unrounded, in fp32.
 //
 // Roles (one persistent CTA per SM, four warpgroups):
 //   warp 0     TMA producer: the tiles' Q, then K and V of each key tile, into
