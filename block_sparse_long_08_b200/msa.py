@@ -748,7 +748,14 @@ def _fits(t, name: str, dtype, numel: int, dev) -> int:
     return t.data_ptr()
 
 
+def _rows(t, name: str, heads: int, d: int):
+    """An input's rows are [heads, d], however many there are."""
+    if t.shape[1:] != (heads, d):
+        raise ValueError(f"{name} must be [rows, {heads}, {d}], got {list(t.shape)}")
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (without its lazy start)
 
 
 def _stream_on(stream, dev):
@@ -763,7 +770,7 @@ def _stream_on(stream, dev):
 def _launch(fn, dev, *args):
     """The call, with the tensors' device as the current one (streams, launches
     and the SM count the library asks for belong to it)."""
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+    if dev.type == "cuda" and dev.index != _current_device():
         with torch.cuda.device(dev):
             rc = fn(*args)
     else:
@@ -840,7 +847,7 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
     inv_freq's length.  Returns q_out (allocated unless given; None without
     q); k_out, when given, receives the rotated keys."""
     _req(k, "k", _BF16)
-    N, G, d = k.shape
+    N, G, d = rows = k.shape
     dev = k.device
     kv = N * G * d
     c, B, L = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G, d, dev)
@@ -853,13 +860,17 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
     H = G
     qa = qo = None
     if q is not None:
-        H = q.shape[1]
+        _, H, dq = q.shape
+        if dq != d:
+            _rows(q, "q", H, d)
         qa = _fits(q, "q", _BF16, N * H * d, dev)
         q_out = _new(lambda: torch.empty_like(q), stream) if q_out is None else q_out
         qo = _fits(q_out, "q_out", _BF16, N * H * d, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     va = _fits(v, "v", _BF16, kv, dev)
+    if v.shape != rows:   # (more rows are fine)
+        _rows(v, "v", G, d)
     la = _fits(seq_lens, "seq_lens", _I32, B, dev)
     cu = None if cu_new is None else _fits(cu_new, "cu_new", _I32, B + 1, dev)
     fa = _fits(inv_freq, "inv_freq", _F32, rot_dim // 2, dev) if rot_dim else None
@@ -880,7 +891,7 @@ def msa_paged_attn_decode(q, k_pages, v_pages, page_table, seq_lens, *, k_scale=
     _req(q, "q", _BF16)
     B, H, d = q.shape
     dev = q.device
-    G = k_pages.shape[2]
+    G = k_pages.shape[2] if k_pages.dim() == 4 else 0   # (else refused below)
     c, Bt, L = _paged_cache(k_pages, v_pages, page_table, k_scale, v_scale, G, d, dev)
     if Bt < B:
         raise ValueError(f"page_table rows: the call needs {B}, there are {Bt}")
@@ -906,6 +917,8 @@ def _dense_inputs(q, k, v, cu_q, cu_k, scale):
     if B < 0:
         raise ValueError("cu_q needs one entry more than there are sequences")
     adr = (q.data_ptr(), _fits(k, "k", _BF16, nk * G * d, dev), _fits(v, "v", _BF16, nk * G * d, dev))
+    _rows(k, "k", G, d)
+    _rows(v, "v", G, d)
     cus = (_fits(cu_q, "cu_q", _I32, 0, dev), _fits(cu_k, "cu_k", _I32, B + 1, dev))
     return nq, nk, _dense_params(B, max(nq, nk), H, G, d, scale), adr, cus, dev
 
@@ -939,6 +952,8 @@ def msa_dense_attn_varlen_backward(q, k, v, out, lse, dout, cu_q, cu_k, *, scale
     dk = _new(lambda: torch.empty_like(k), stream) if dk is None else dk
     dv = _new(lambda: torch.empty_like(v), stream) if dv is None else dv
     oa, da, qa = (_fits(t, n, _BF16, q.numel(), dev) for n, t in (("out", out), ("dout", dout), ("dq", dq)))
+    for n, x in (("out", out), ("dout", dout)):
+        _rows(x, n, q.shape[1], q.shape[2])
     ka, va = (_fits(t, n, _BF16, nkv, dev) for n, t in (("dk", dk), ("dv", dv)))
     ea = _fits(lse, "lse", _F32, nq * q.shape[1], dev)
     ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN_BACKWARD, dev, stream)

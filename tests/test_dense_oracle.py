@@ -228,3 +228,24 @@ def test_binding_refuses_two_devices(stub):  # noqa: F811
     q, k = torch.zeros(4, 8, 128, dtype=BF16), torch.zeros(4, 2, 128, dtype=BF16)
     cu = torch.tensor([0, 4], dtype=torch.int32)
     _refused(stub, M.msa_dense_attn_varlen, q, k, k.to("meta"), cu, cu, match="is on meta")
+
+
+def test_binding_refuses_rows_of_another_shape(stub):  # noqa: F811
+    """Enough elements in all, but not the rows the call would read."""
+    q, k = torch.zeros(10, 8, 128, dtype=BF16), torch.zeros(12, 2, 128, dtype=BF16)
+    cq, ck = torch.tensor([0, 10], dtype=torch.int32), torch.tensor([0, 12], dtype=torch.int32)
+    out, lse = torch.zeros_like(q), torch.zeros(10, 8)
+    wide, turned = torch.zeros(12, 2, 256, dtype=BF16), torch.zeros(8, 10, 128, dtype=BF16)
+    fwd, bwd = M.msa_dense_attn_varlen, M.msa_dense_attn_varlen_backward
+    _refused(stub, fwd, q, wide, wide, cq, ck, match="k must be")
+    _refused(stub, fwd, q, k, wide, cq, ck, match="v must be")
+    _refused(stub, fwd, q, k, k.reshape(12, 256), cq, ck, match="v must be")
+    _refused(stub, bwd, q, k, k, out, lse, turned, cq, ck, match="dout must be")
+    _refused(stub, bwd, q, k, k, turned, lse, out, cq, ck, match="out must be")
+    pages, table = torch.zeros(9, 32, 2, 128, dtype=BF16), torch.zeros(3, 3, dtype=torch.int32)
+    lens, k3 = torch.ones(3, dtype=torch.int32), torch.zeros(3, 2, 128, dtype=BF16)
+    _refused(stub, M.msa_paged_append, k3, torch.zeros(3, 4, 128, dtype=BF16), pages, pages, table, lens,
+             match="v must be")
+    _refused(stub, M.msa_paged_append, k3, k3, pages, pages, table, lens, q=torch.zeros(3, 8, 256, dtype=BF16),
+             match="q must be")
+    _refused(stub, M.msa_paged_attn_decode, q[:3], pages[0], pages[0], table, lens, match="k_pages, v_pages must")
