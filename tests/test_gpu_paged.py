@@ -455,3 +455,27 @@ def test_decode_nan_stays_with_its_head(G, R, lens, fp8):
         else:
             assert torch.equal(ls[hit], lse[hit])
         assert torch.equal(ls[~hit], lse[~hit])
+
+
+def test_append_fp8_codes_are_those_of_the_quotient():
+    """Every bf16 significand as a row's largest value, against every other one
+    at twelve powers of two: each code is that of x / scale (92 of these
+    quotients lie so near the middle of two codes that x times 1 / scale
+    would get the other one)."""
+    page, m = 64, torch.arange(128.0, 256.0)
+    x = torch.stack([torch.minimum(m[None] * 2.0 ** -j, m[:, None]) for j in range(12)])   # [12, largest, 128]
+    x[..., 127] = m                               # (255 2^-j gives way to the largest)
+    n = 12 * 128 // 4
+    k = x.view(n, 4, 128).to(BF16)
+    assert torch.equal(k.float(), x.view(n, 4, 128))
+    kp, vp = (torch.zeros(n // page, page, 4, 128, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros(n // page, page, 4, device=DEV) for _ in range(2))
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).reshape(1, -1)
+    M.msa_paged_append(k.to(DEV), -k.to(DEV), kp, vp, table, torch.tensor([n], dtype=torch.int32, device=DEV),
+                       cu_new=torch.tensor([0, n], dtype=torch.int32, device=DEV), k_scale=ks, v_scale=vs)
+    scale = k.float().abs().amax(-1) / 448
+    want = (k.float() / scale[..., None]).to(torch.float8_e4m3fn).float()
+    for codes, sc, sign in ((kp, ks, 1.0), (vp, vs, -1.0)):
+        assert torch.equal(sc.view(n, 4).cpu(), scale)
+        got = codes.view(n, 4, 128).cpu().view(torch.float8_e4m3fn).float()
+        assert torch.equal(got, sign * want)
