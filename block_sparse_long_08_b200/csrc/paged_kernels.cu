@@ -241,7 +241,8 @@ struct PdCfg {
   static constexpr int OFF_O = 4 * WARP;       // [R][128] fp32
   static constexpr int OFF_ML = OFF_O + R * kHeadDim * 4;   // [4][16] maxima, [4][16] sums
   static constexpr int OFF_VIS = OFF_ML + 2 * 4 * 16 * 4;   // [4][NST] visible keys
-  static constexpr int SMEM = OFF_VIS + 4 * NST * 4;
+  static constexpr int OFF_SL = OFF_VIS + 4 * NST * 4;   // [4][16] factors of the heads' scores (8-bit, not KM)
+  static constexpr int SMEM = OFF_SL + 256;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 };
 
@@ -287,10 +288,16 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(in));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t w) {
-  const __half2 h = __floats2half2_rn(bf16_lo(w), bf16_hi(w));
+// Two bf16 values times f as two f16 values.
+__device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t w, float f) {
+  const __half2 h = __floats2half2_rn(bf16_lo(w) * f, bf16_hi(w) * f);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
+// The exponent field of the power of two that brings x into [2^14, 2^15), at most
+// 2^112: what a query row is multiplied by before it is rounded to f16, so that
+// f16 holds rows of any size (elements down to 2^-28 of the row's largest keep
+// their bits, the others are off by 2^-39 of it).  2^(254 - field - 127) undoes it.
+__device__ __forceinline__ uint32_t f16_lift(float x) { return min(268u - (__float_as_uint(x) >> 23), 239u); }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -418,6 +425,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
     uint8_t *smp = dsm + warp * C::WARP;
     float *s_m = reinterpret_cast<float *>(dsm + C::OFF_ML), *s_l = s_m + 64;
     volatile int *s_vis = reinterpret_cast<volatile int *>(dsm + C::OFF_VIS) + warp * C::NST;
+    volatile float *s_sl = reinterpret_cast<volatile float *>(dsm + C::OFF_SL) + warp * 16;
     const int pmask = (1 << a.c.page_log2) - 1;
     PdCur ld;
     ld.b = s_start[0]; ld.t = s_start[1];
@@ -499,6 +507,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     uint32_t qf[8][4];
+    float sl0 = 0.f, sl1 = 0.f;                     // KM: a.scale_log2 with the lift of this lane's heads undone
     bool fresh = true;                              // a new pair: its queries are to be loaded
     bool head = cu.t > 0;                           // the pair began in an earlier run
     int pair_left = 0;
@@ -518,8 +527,36 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
             const int d = FP8 ? 16 * (c + 4 * (kk >> 2)) + 4 * (kk & 3) + (e >> 1) * 2 : kk * 16 + 2 * c + (e >> 1) * 8;
             uint32_t w = 0;
             if (r < R) w = *reinterpret_cast<const uint32_t *>(a.q + (size_t(cu.b) * a.H + g * R + r) * kHeadDim + d);
-            qf[kk][e] = FP8 ? f16x2_of_bf16x2(w) : w;
+            qf[kk][e] = w;
           }
+        if (FP8) {   // to f16, each head's row lifted by its own power of two
+          float x[2] = {0.f, 0.f};
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!C::KM || !(e & 1))
+                x[e & 1] = fmaxf(x[e & 1], fmaxf(fabsf(bf16_lo(qf[kk][e])), fabsf(bf16_hi(qf[kk][e]))));
+#pragma unroll
+          for (int i = 1; i < 4; i <<= 1) {
+            x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], i));
+            if (!C::KM) x[1] = fmaxf(x[1], __shfl_xor_sync(0xffffffffu, x[1], i));
+          }
+          const uint32_t up[2] = {f16_lift(x[0]), f16_lift(x[1])};
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!C::KM || !(e & 1)) qf[kk][e] = f16x2_of_bf16x2(qf[kk][e], __uint_as_float(up[e & 1] << 23));
+          const float d0 = __uint_as_float((254u - up[0]) << 23) * a.scale_log2;
+          const float d1 = __uint_as_float((254u - up[1]) << 23) * a.scale_log2;
+          // KM: this lane loaded head g4, its scores are of heads 2c and 2c + 1.
+          // Else through shared memory: the sixteen-head form has no two registers
+          // to spare (kept there it spills: 16 x 32K tokens 170 us, 149 this way)
+          sl0 = __shfl_sync(0xffffffffu, d0, 8 * c);
+          sl1 = __shfl_sync(0xffffffffu, d0, 8 * c + 4);
+          if (!C::KM && c == 0) { s_sl[g4] = d0; s_sl[g4 + 8] = d1; }
+        }
       }
       cpa_wait<C::NST - 2>();
       __syncwarp();
@@ -542,9 +579,10 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
             mma_f16(s, ka, qf[4 * h + x][0], qf[4 * h + x][2]);
           }
         }
-        const float k0 = sc[g4] * a.scale_log2, k1 = sc[g4 + 8] * a.scale_log2;
+        const float k0 = sc[g4], k1 = sc[g4 + 8];
         const float v0 = sc[16 + g4], v1 = sc[24 + g4];
-        s[0] *= k0; s[1] *= k0; s[2] *= k1; s[3] *= k1;     // log2 units
+        // log2 units (the factors first: the scale brings the lift's undoing back into range)
+        s[0] *= k0 * sl0; s[1] *= k0 * sl1; s[2] *= k1 * sl0; s[3] *= k1 * sl1;
         if (vis < 16) {
           if (g4 >= vis) s[0] = s[1] = -INFINITY;
           if (g4 + 8 >= vis) s[2] = s[3] = -INFINITY;
@@ -607,6 +645,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
           }
       }
       if (!C::KM && vis > 0) {
+        const float unit = FP8 ? 1.f : a.scale_log2;   // of the scores below, in log2
         float s[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -632,7 +671,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
           for (int i = 0; i < 2; ++i) {
             const float2 k2 = *reinterpret_cast<const float2 *>(sc + i * 8 + 2 * c);
             const float2 v2 = *reinterpret_cast<const float2 *>(sc + 16 + i * 8 + 2 * c);
-            s[i][0] *= k2.x; s[i][1] *= k2.y; s[i][2] *= k2.x; s[i][3] *= k2.y;
+            const float f0 = s_sl[g4], f1 = s_sl[g4 + 8];   // (log2 units, as above)
+            s[i][0] *= k2.x * f0; s[i][1] *= k2.y * f0; s[i][2] *= k2.x * f1; s[i][3] *= k2.y * f1;
             vs[i][0] = v2.x; vs[i][1] = v2.y;
           }
           // V's codes as f16 rows in the scratch: the two granules that a
@@ -678,11 +718,11 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         }
         if (R <= 8) x1 = m1;   // rows 8-15 hold no head: their zeros move nothing
         // (a step with a visible key has a finite maximum, so m0 and m1 are finite behind it)
-        const bool up0 = m0 == -INFINITY || (x0 - m0) * a.scale_log2 > 8.f;
-        const bool up1 = R > 8 && (m1 == -INFINITY || (x1 - m1) * a.scale_log2 > 8.f);
+        const bool up0 = m0 == -INFINITY || (x0 - m0) * unit > 8.f;
+        const bool up1 = R > 8 && (m1 == -INFINITY || (x1 - m1) * unit > 8.f);
         if (__any_sync(0xffffffffu, up0 || up1)) {
-          const float al0 = up0 ? (m0 == -INFINITY ? 0.f : exp2_fast((m0 - x0) * a.scale_log2)) : 1.f;
-          const float al1 = up1 ? (m1 == -INFINITY ? 0.f : exp2_fast((m1 - x1) * a.scale_log2)) : 1.f;
+          const float al0 = up0 ? (m0 == -INFINITY ? 0.f : exp2_fast((m0 - x0) * unit)) : 1.f;
+          const float al1 = up1 ? (m1 == -INFINITY ? 0.f : exp2_fast((m1 - x1) * unit)) : 1.f;
           if (up0) m0 = x0;
           if (up1) m1 = x1;
           l0 *= al0;
@@ -695,7 +735,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
             }
           }
         }
-        const float n0 = -m0 * a.scale_log2, n1 = R > 8 ? -m1 * a.scale_log2 : 0.f;
+        const float n0 = -m0 * unit, n1 = R > 8 ? -m1 * unit : 0.f;
         uint32_t pa[4];
         float lv[2][2], w0 = 0.f, w1 = 0.f;
         if (FP8) {
@@ -707,8 +747,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               lv[i][e] = __log2f(fabsf(vs[i][e]));
-              y0 = fmaxf(y0, fmaf(s[i][e], a.scale_log2, lv[i][e]));
-              if (R > 8) y1 = fmaxf(y1, fmaf(s[i][2 + e], a.scale_log2, lv[i][e]));
+              y0 = fmaxf(y0, fmaf(s[i][e], unit, lv[i][e]));
+              if (R > 8) y1 = fmaxf(y1, fmaf(s[i][2 + e], unit, lv[i][e]));
             }
 #pragma unroll
           for (int i = 1; i < 4; i <<= 1) {
@@ -735,7 +775,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int h = 0; h < (R > 8 ? 2 : 1); ++h) {   // rows g4, then g4 + 8
-            const float z0 = s[i][2 * h] * a.scale_log2, z1 = s[i][2 * h + 1] * a.scale_log2;
+            const float z0 = s[i][2 * h] * unit, z1 = s[i][2 * h + 1] * unit;
             const float n = h ? n1 : n0, w = h ? w1 : w0;
             const float p0 = exp2_fast(z0 + n), p1 = exp2_fast(z1 + n);
             if (h) l1 += p0 + p1; else l0 += p0 + p1;
@@ -778,7 +818,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
           l0 += __shfl_xor_sync(0xffffffffu, l0, i);
           l1 += __shfl_xor_sync(0xffffffffu, l1, i);
         }
-        if (C::KM) {   // from log2 units back to those of the scores
+        if (FP8) {   // from log2 units back to those of the scores
           m0 /= a.scale_log2;
           m1 /= a.scale_log2;
         }

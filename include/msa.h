@@ -483,8 +483,10 @@ int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, 
  * parts of one sequence joined by a second launch (short calls: within one);
  * the split depends on the lengths and p alone, so results repeat bit for
  * bit.
- * An 8-bit cache's scores run in f16 (|q| < 65504); each value's scale is
- * folded into its softmax weight before the weight is rounded to f16.
+ * An 8-bit cache's scores multiply its codes by the query in f16, each row
+ * lifted by a power of two first: elements down to 2^-28 of the row's largest
+ * keep their bits, smaller ones are off by up to 2^-39 of it.  Each value's
+ * scale is folded into its softmax weight before the weight is rounded to f16.
  * ws >= msa_workspace_bytes(p, MSA_OP_PAGED_DECODE). */
 int msa_paged_attn_decode(const msa_params *p, const msa_paged_cache *c, const msa_bf16 *q,
                           const int32_t *seq_lens, msa_bf16 *out, float *lse, void *ws,

@@ -479,3 +479,22 @@ def test_append_fp8_codes_are_those_of_the_quotient():
         assert torch.equal(sc.view(n, 4).cpu(), scale)
         got = codes.view(n, 4, 128).cpu().view(torch.float8_e4m3fn).float()
         assert torch.equal(got, sign * want)
+
+
+@pytest.mark.parametrize("cols", [20, 300])       # the one-launch form and the split one
+@pytest.mark.parametrize("G,R", [(2, 4), (2, 8), (2, 1), (2, 16)])
+@pytest.mark.parametrize("gain", [1e-9, 1e-5, 1e-35, 1e7, 1e35])
+def test_decode_fp8_queries_of_any_size(gain, G, R, cols):
+    """Queries far under and over what f16 holds, against keys whose scales
+    bring the scores back (KV head 0); beside them (1) heads of every size;
+    and elements of every size within a row."""
+    lens = [300, 33]
+    c = make_cache(lens, G, 16, True, seed=51, cols=cols)
+    c["ks"][..., 0] /= gain
+    q = torch.randn(2, G, R, 128, generator=torch.Generator().manual_seed(6))
+    q[1] *= 2.0 ** -torch.arange(128).div(8, rounding_mode="floor")
+    q[:, 0] *= gain
+    q[0, 1] *= 2.0 ** -(3.0 * torch.arange(R))[:, None]
+    q = q.view(2, G * R, 128).to(BF16).to(DEV)
+    out, lse = decode(c, q, lens)
+    check_decode(c, q, lens, out, lse)
