@@ -218,11 +218,16 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendA
 //   Sums    Per warp a running maximum, moved when a step exceeds it by more
 //           than 2^8 in P, and a sum, both fp32; P is rounded to bf16 for the
 //           product with V (8-bit: P times the value's scale to f16, the
-//           codes' own type in the product).
+//           codes' own type in the product, against a reference of its own
+//           that lets the weights run up to 2^15: f16 keeps their 11 bits down
+//           to 2^-25 of the largest, and none above 2^-36 of it is lost).
 constexpr int kPdTile = 64;                 // keys per tile, 16 per warp
 constexpr int kPdThreads = 128;
 constexpr int kPdMaxGrid = 1024;            // CTAs, and so parts, at most
 constexpr int kPdRow = kHeadDim + 2;        // floats per head of a part: O, maximum, sum
+// 8-bit: the reference of the weights is moved when one passes 2^kPdWTop, to
+// where it is 2^kPdWRef.
+constexpr float kPdWTop = 15.f, kPdWRef = 11.f;
 
 template <int R, bool FP8>
 struct PdCfg {
@@ -600,15 +605,15 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         // two references as below: m for the sums, mw for the weights that
         // multiply V's codes (P |scale|, f16); both in log2 units here
         const bool up0 = m0 == -INFINITY || x0 - m0 > 8.f, up1 = m1 == -INFINITY || x1 - m1 > 8.f;
-        const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > 8.f);
-        const bool wu1 = y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > 8.f);
+        const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > kPdWTop);
+        const bool wu1 = y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > kPdWTop);
         if (__any_sync(0xffffffffu, up0 || up1 || wu0 || wu1)) {
           if (up0) { l0 *= m0 == -INFINITY ? 0.f : exp2_fast(m0 - x0); m0 = x0; }
           if (up1) { l1 *= m1 == -INFINITY ? 0.f : exp2_fast(m1 - x1); m1 = x1; }
-          const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - y0)) : 1.f;
-          const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - y1)) : 1.f;
-          if (wu0) mw0 = y0;
-          if (wu1) mw1 = y1;
+          const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - (y0 - kPdWRef))) : 1.f;
+          const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - (y1 - kPdWRef))) : 1.f;
+          if (wu0) mw0 = y0 - kPdWRef;
+          if (wu1) mw1 = y1 - kPdWRef;
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
             o[d][0] *= al0; o[d][2] *= al0;
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         float lv[2][2], w0 = 0.f, w1 = 0.f;
         if (FP8) {
           // the weights that multiply V's codes are P |scale|, in f16, against
-          // a reference of their own (log2): any scale keeps its 11 bits
+          // a reference of their own (log2), whatever the scales
           float y0 = -INFINITY, y1 = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -755,13 +760,13 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
             y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, i));
             if (R > 8) y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, i));
           }
-          const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > 8.f);
-          const bool wu1 = R > 8 && y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > 8.f);
+          const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > kPdWTop);
+          const bool wu1 = R > 8 && y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > kPdWTop);
           if (__any_sync(0xffffffffu, wu0 || wu1)) {
-            const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - y0)) : 1.f;
-            const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - y1)) : 1.f;
-            if (wu0) mw0 = y0;
-            if (wu1) mw1 = y1;
+            const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - (y0 - kPdWRef))) : 1.f;
+            const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - (y1 - kPdWRef))) : 1.f;
+            if (wu0) mw0 = y0 - kPdWRef;
+            if (wu1) mw1 = y1 - kPdWRef;
 #pragma unroll
             for (int d = 0; d < 16; ++d) {
               o[d][0] *= al0; o[d][1] *= al0;

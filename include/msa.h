@@ -486,7 +486,8 @@ int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, 
  * An 8-bit cache's scores multiply its codes by the query in f16, each row
  * lifted by a power of two first: elements down to 2^-28 of the row's largest
  * keep their bits, smaller ones are off by up to 2^-39 of it.  Each value's
- * scale is folded into its softmax weight before the weight is rounded to f16.
+ * scale is folded into its softmax weight before the weight is rounded to f16:
+ * by 2^-11 of it, or 2^-36 of the largest where that is more.
  * ws >= msa_workspace_bytes(p, MSA_OP_PAGED_DECODE). */
 int msa_paged_attn_decode(const msa_params *p, const msa_paged_cache *c, const msa_bf16 *q,
                           const int32_t *seq_lens, msa_bf16 *out, float *lse, void *ws,

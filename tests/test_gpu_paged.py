@@ -498,3 +498,30 @@ def test_decode_fp8_queries_of_any_size(gain, G, R, cols):
     q = q.view(2, G * R, 128).to(BF16).to(DEV)
     out, lse = decode(c, q, lens)
     check_decode(c, q, lens, out, lse)
+
+
+@pytest.mark.parametrize("G,R,lens,cols", [(2, 4, [300, 33], 20), (2, 16, [300, 33], 20), (1, 4, [5000, 70], 330),
+                                           (1, 16, [5000, 70], 330), (1, 8, [90000], 5630)])
+def test_decode_fp8_tail_behind_sinks(G, R, lens, cols):
+    """Every sixteenth key takes nearly all of the weight and has a value of
+    zero: what comes out is the others' share, 2^-26 of it each."""
+    c = make_cache(lens, G, 16, True, seed=52, cols=cols)
+    gen = torch.Generator().manual_seed(7)
+    own, shape = c["own"], c["k"].shape
+    k0 = torch.randint(-1, 2, shape[:3], generator=gen).float() / 4
+    v = torch.randn(shape, generator=gen).abs() + 0.5
+    sink = torch.zeros(shape[:3], dtype=torch.bool)
+    sink[:, 3] = True
+    k0[sink], v[sink] = 18.0, 0.0                  # e^-18 = 2^-25.97
+    k = c["k"].cpu().view(torch.float8_e4m3fn).float()
+    k[..., 0] = k0
+    for x, t in (("k", k), ("v", v)):
+        codes = t.to(torch.float8_e4m3fn).view(torch.uint8)
+        codes[~own] = 0x7F
+        c[x] = codes.to(DEV)
+    c["ks"] = torch.where(own[..., None], 1.0, float("nan")).expand(shape[:3]).contiguous().to(DEV)
+    q = torch.zeros(len(lens), G * R, 128, device=DEV, dtype=BF16)
+    q[..., 0] = 1.0
+    out, lse = decode(c, q, lens, scale=1.0)
+    check_decode(c, q, lens, out, lse, scale=1.0)
+    assert (out[0] > 0).all()
