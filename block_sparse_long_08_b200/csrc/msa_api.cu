@@ -652,6 +652,16 @@ bool dense_op(int op) { return op >= MSA_OP_PAGED_APPEND && op <= MSA_OP_DENSE_V
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Bytes [p, p + n) of a call's tensor.
+struct Span {
+  const void *p;
+  size_t n;
+};
+bool overlap(const Span &x, const Span &y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.n && y.n && a < b + y.n && b < a + x.n;
+}
+
 // Packed-sequence operations: {q0, nq, k0, nk} per sequence, the count, the
 // prefix and the list of its work items (as many as p->L packed query rows
 // and one more per sequence can make); for the backward also those of its
@@ -1458,6 +1468,16 @@ int msa_dense_attn_varlen_backward(const msa_params *p, int nq, int nk, const ms
   if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return fail(MSA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   if (nq == 0 && nk == 0) return MSA_OK;
+  // dq's kernel reads q, k, v and dout while dk's and dv's still runs, and the other way round
+  const size_t bq = size_t(nq) * p->H * p->d * 2, bk = size_t(nk) * p->G * p->d * 2;
+  const Span in[4] = {{q, bq}, {dout, bq}, {k, bk}, {v, bk}}, res[3] = {{dq, bq}, {dk, bk}, {dv, bk}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span &x : in)
+      if (overlap(res[i], x))
+        return fail(MSA_ERR_INVALID_ARG, "dq, dk and dv must not overlap q, k, v or dout");
+    for (int j = 0; j < i; ++j)
+      if (overlap(res[i], res[j])) return fail(MSA_ERR_INVALID_ARG, "dq, dk and dv must not overlap");
+  }
   a.out = const_cast<msa_bf16 *>(out);
   a.lse = const_cast<float *>(lse);
   a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv;

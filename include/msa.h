@@ -419,6 +419,7 @@ int msa_nsa_forward(const msa_params *p, int32_t window, const msa_bf16 *q, cons
  * kernels run, so a captured call serves other lengths when it is replayed.
  * Calls whose work may overlap (two streams, two graphs) need a workspace
  * each.
+ * Results overlap neither inputs nor each other, but where a call says so.
  *
  * A paged cache.  Token t of sequence b lives in row t % page_size of page
  * page_table[b][t / page_size], one table for keys and values. */
@@ -519,7 +520,10 @@ int msa_dense_attn_varlen(const msa_params *p, int nq, int nk, const msa_bf16 *q
  * dq = scale sum_s dZ_s k_s, dk_s += scale dZ_s q, dv_s += P_s dout over the
  * rows and heads of the group that see s.  Keys no query sees, and queries
  * that see no key, get zeros.  Rows behind cu_q[B] and cu_k[B] are left as
- * they were; bit-identical from run to run.
+ * they were; bit-identical from run to run.  A sequence's own rows of q, k, v,
+ * dout, out and lse are finite (lse -inf where no key is seen); rows of other
+ * sequences and rows behind the last one may hold anything.  dq, dk and dv
+ * overlap neither each other nor q, k, v or dout.
  * ws >= msa_workspace_bytes(p, MSA_OP_DENSE_VARLEN_BACKWARD). */
 int msa_dense_attn_varlen_backward(const msa_params *p, int nq, int nk, const msa_bf16 *q,
                                    const msa_bf16 *k, const msa_bf16 *v, const msa_bf16 *out,

@@ -249,3 +249,25 @@ def test_binding_refuses_rows_of_another_shape(stub):  # noqa: F811
     _refused(stub, M.msa_paged_append, k3, k3, pages, pages, table, lens, q=torch.zeros(3, 8, 256, dtype=BF16),
              match="q must be")
     _refused(stub, M.msa_paged_attn_decode, q[:3], pages[0], pages[0], table, lens, match="k_pages, v_pages must")
+
+
+def test_backward_refuses_results_over_what_it_reads():
+    """Two kernels run at once: no gradient may lie over an input of the other
+    one, or over another gradient."""
+    p = M.make_params(1, 10, 8, 2)
+    big, small = 10 * 8 * 128 * 2, 10 * 2 * 128 * 2
+    at = {n: (i + 1) << 20 for i, n in enumerate(("q", "k", "v", "out", "lse", "dout", "cq", "ck", "dq", "dk", "dv", "ws"))}
+
+    def call(**kw):
+        a = {n: ctypes.c_void_p(x) for n, x in {**at, **kw}.items()}
+        return M.lib().msa_dense_attn_varlen_backward(
+            ctypes.byref(p), 10, 10, a["q"], a["k"], a["v"], a["out"], a["lse"], a["dout"], a["cq"], a["ck"],
+            a["dq"], a["dk"], a["dv"], a["ws"], 1 << 20, None)
+    sizes = {"q": big, "dout": big, "k": small, "v": small, "dq": big, "dk": small, "dv": small}
+    for res in ("dq", "dk", "dv"):
+        for other in sizes:
+            if other == res:
+                continue
+            for x in (at[other], at[other] + sizes[other] - 16, at[other] - sizes[res] + 16):
+                assert call(**{res: x}) == M.MSA_ERR_INVALID_ARG, (res, other)
+                assert "overlap" in M.msa_last_error()
