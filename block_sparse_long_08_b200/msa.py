@@ -732,6 +732,11 @@ def msa_sparse_attn_decode_noalloc(q, q_idx, k_cache, v_cache, k_idx_cache, seq_
 # check each tensor in one expression and name what is wrong only when it
 # fails, pass addresses as plain integers, and leave the size of a given
 # workspace to the library's own check.
+#
+# What the kernels refuse on the device (lengths, starts and page ids out of
+# range) only shows in the status word of the workspace: a caller who wants to
+# know passes `ws` and asks msa_read_status.  Without `ws`, the rows that such a
+# call skips are zeros in the results it allocates.
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
@@ -793,6 +798,16 @@ def _new(make, stream):
         return make()
 
 
+def _result(t, shape, dtype, dev, ws, stream):
+    """A result that a call on the device may skip rows of: the caller's, or
+    allocated.  Without a workspace of the caller's nobody can read the
+    status word, so rows that are skipped (a batch that is refused, rows no
+    sequence owns) are zeros then and not what the memory held before."""
+    if t is not None:
+        return t
+    return _new(lambda: (torch.zeros if ws is None else torch.empty)(shape, dtype=dtype, device=dev), stream)
+
+
 def _call_ws(ws, p, op, dev, stream):
     """(workspace, its address and size): allocated for the call when None."""
     if ws is None:
@@ -845,7 +860,9 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
     page_table [B,cols], seq_lens [B] (new tokens included), cu_new [B+1]
     (None: one row per sequence), all int32.  rot_dim defaults to twice
     inv_freq's length.  Returns q_out (allocated unless given; None without
-    q); k_out, when given, receives the rotated keys."""
+    q); k_out, when given, receives the rotated keys.  Rows that are skipped
+    (padding, refused on the device) keep what q_out held: zeros when the call
+    allocates it and ws."""
     _req(k, "k", _BF16)
     N, G, d = rows = k.shape
     dev = k.device
@@ -864,7 +881,7 @@ def msa_paged_append(k, v, k_pages, v_pages, page_table, seq_lens, *, cu_new=Non
         if dq != d:
             _rows(q, "q", H, d)
         qa = _fits(q, "q", _BF16, N * H * d, dev)
-        q_out = _new(lambda: torch.empty_like(q), stream) if q_out is None else q_out
+        q_out = _result(q_out, q.shape, _BF16, dev, ws, stream)
         qo = _fits(q_out, "q_out", _BF16, N * H * d, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -928,13 +945,14 @@ def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: 
     """Dense causal attention over packed sequences: q [nq,H,d], k, v
     [nk,G,d], cu_q and cu_k [B+1] int32 (device), queries aligned to the end
     of their sequence's keys -> out [nq,H,d] (and lse [nq,H] when want_lse or
-    given).  Rows behind cu_q[B] are left as they were."""
+    given).  Rows behind cu_q[B] are left as they were, all rows when the batch
+    is refused on the device (zeros in what a call without ws allocates)."""
     nq, nk, p, adr, cus, dev = _dense_inputs(q, k, v, cu_q, cu_k, scale)
     H = q.shape[1]
-    out = _new(lambda: torch.empty_like(q), stream) if out is None else out
+    out = _result(out, q.shape, _BF16, dev, ws, stream)
     oa = _fits(out, "out", _BF16, q.numel(), dev)
-    if lse is None and want_lse:
-        lse = _new(lambda: torch.empty((nq, H), dtype=_F32, device=dev), stream)
+    if lse is not None or want_lse:
+        lse = _result(lse, (nq, H), _F32, dev, ws, stream)
     ea = None if lse is None else _fits(lse, "lse", _F32, nq * H, dev)
     ws, wa, wn = _call_ws(ws, p, MSA_OP_DENSE_VARLEN, dev, stream)
     _launch(lib().msa_dense_attn_varlen, dev, ctypes.byref(p), nq, nk, *adr, *cus, oa, ea, wa, wn,
@@ -945,12 +963,13 @@ def msa_dense_attn_varlen(q, k, v, cu_q, cu_k, *, scale: float = 0.0, want_lse: 
 def msa_dense_attn_varlen_backward(q, k, v, out, lse, dout, cu_q, cu_k, *, scale: float = 0.0,
                                    dq=None, dk=None, dv=None, ws=None, stream=None):
     """Gradients of msa_dense_attn_varlen: its inputs, its out [nq,H,d] and lse
-    [nq,H], dout [nq,H,d] -> (dq, dk, dv) bf16, shaped like q, k, v."""
+    [nq,H], dout [nq,H,d] -> (dq, dk, dv) bf16, shaped like q, k, v.  Rows that
+    no sequence owns, all rows when the batch is refused, as in the forward."""
     nq, nk, p, adr, cus, dev = _dense_inputs(q, k, v, cu_q, cu_k, scale)
     nkv = nk * k.shape[1] * k.shape[2]
-    dq = _new(lambda: torch.empty_like(q), stream) if dq is None else dq
-    dk = _new(lambda: torch.empty_like(k), stream) if dk is None else dk
-    dv = _new(lambda: torch.empty_like(v), stream) if dv is None else dv
+    dq = _result(dq, q.shape, _BF16, dev, ws, stream)
+    dk = _result(dk, k.shape, _BF16, dev, ws, stream)
+    dv = _result(dv, v.shape, _BF16, dev, ws, stream)
     oa, da, qa = (_fits(t, n, _BF16, q.numel(), dev) for n, t in (("out", out), ("dout", dout), ("dq", dq)))
     for n, x in (("out", out), ("dout", dout)):
         _rows(x, n, q.shape[1], q.shape[2])

@@ -271,3 +271,21 @@ def test_backward_refuses_results_over_what_it_reads():
             for x in (at[other], at[other] + sizes[other] - 16, at[other] - sizes[res] + 16):
                 assert call(**{res: x}) == M.MSA_ERR_INVALID_ARG, (res, other)
                 assert "overlap" in M.msa_last_error()
+
+
+def test_binding_allocates_zeros_where_rows_may_be_skipped(stub, monkeypatch):  # noqa: F811
+    """Nothing of older memory in a result that the call allocates together
+    with its workspace; a caller's buffers are left alone."""
+    fill = torch.full
+    monkeypatch.setattr(M.torch, "empty", lambda *a, **kw: fill(a[0] if len(a) == 1 else a, 7, **kw))
+    monkeypatch.setattr(M.torch, "empty_like", lambda t, **kw: fill(t.shape, 7, dtype=t.dtype))
+    q, k = torch.zeros(10, 8, 128, dtype=BF16), torch.zeros(12, 2, 128, dtype=BF16)
+    cq, ck = torch.tensor([0, 4, 10], dtype=torch.int32), torch.tensor([0, 6, 12], dtype=torch.int32)
+    res = M.msa_dense_attn_varlen(q, k, k, cq, ck, want_lse=True)
+    res += M.msa_dense_attn_varlen_backward(q, k, k, q, res[1], q, cq, ck)
+    pages, table = torch.zeros(9, 32, 2, 128, dtype=BF16), torch.zeros(3, 3, dtype=torch.int32)
+    lens = torch.ones(3, dtype=torch.int32)
+    res += (M.msa_paged_append(k[:3], k[:3], pages, pages, table, lens, q=q[:3]),)
+    assert len(res) == 6 and all((t == 0).all() for t in res)
+    mine = fill(q.shape, 3.0, dtype=BF16)
+    assert M.msa_dense_attn_varlen(q, k, k, cq, ck, out=mine) is mine and (mine == 3).all()

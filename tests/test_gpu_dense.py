@@ -403,3 +403,21 @@ def test_what_a_call_allocates_belongs_to_the_given_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, (out, lse) + tuple(grads) + (one,)))
     assert all((j == 255).all() for j in junk)
+
+
+def test_a_refused_batch_without_a_workspace_gives_zeros():
+    """Results that the call allocates hold nothing of older memory."""
+    x, _, _ = packed([50, 50], [50, 50], 1, 2)
+    cq, ck = i32([0, 60, 50]), i32([0, 50, 100])
+    for _ in range(3):
+        junk = [torch.full_like(x[n], 7.0) for n in ("q", "q", "k", "k", "k")] + [torch.full((100, 2), 7.0, device=DEV)]
+        del junk
+        out, lse = M.msa_dense_attn_varlen(x["q"], x["k"], x["v"], cq, ck, want_lse=True)
+        assert (out == 0).all() and (lse == 0).all()
+        del out, lse
+        out, lse = torch.zeros_like(x["q"]), torch.zeros(100, 2, device=DEV)
+        junk = [torch.full_like(x[n], 7.0) for n in ("q", "q", "k", "k", "k")]
+        del junk
+        grads = M.msa_dense_attn_varlen_backward(x["q"], x["k"], x["v"], out, lse, x["dout"], cq, ck)
+        assert all((t == 0).all() for t in grads)
+        del grads

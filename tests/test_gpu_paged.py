@@ -525,3 +525,18 @@ def test_decode_fp8_tail_behind_sinks(G, R, lens, cols):
     out, lse = decode(c, q, lens, scale=1.0)
     check_decode(c, q, lens, out, lse, scale=1.0)
     assert (out[0] > 0).all()
+
+
+def test_bad_pages_and_lengths_without_a_workspace_give_zeros():
+    """A call that allocates its results and its workspace leaves nothing of
+    older memory in rows that it skips."""
+    junk = [torch.full((2 ** i,), 7.0, dtype=BF16, device=DEV) for i in range(6, 16) for _ in range(3)]
+    del junk
+    k = torch.ones(4, 1, 128, dtype=BF16, device=DEV)
+    pages = [torch.zeros(4, 16, 1, 128, dtype=BF16, device=DEV) for _ in range(2)]
+    table = torch.tensor([[0], [9]], dtype=torch.int32, device=DEV)
+    n = torch.tensor([2, 2], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
+    q = torch.ones(4, 4, 128, dtype=BF16, device=DEV)
+    out = M.msa_paged_append(k, k, *pages, table, n, cu_new=cu, q=q)
+    assert (out[:2] == 1).all() and (out[2:] == 0).all()
