@@ -482,8 +482,8 @@ int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, 
  * a page whose id lies outside [0, num_pages) are left out and set it too.
  * The cache's tokens are shared out over the SMs whatever the lengths, the
  * parts of one sequence joined by a second launch (short calls: within one);
- * the split depends on the lengths and p alone, so results repeat bit for
- * bit.
+ * the split depends on the lengths, p and the device's number of SMs alone,
+ * so results repeat bit for bit on one kind of device.
  * An 8-bit cache's scores multiply its codes by the query in f16, each row
  * lifted by a power of two first: elements down to 2^-28 of the row's largest
  * keep their bits, smaller ones are off by up to 2^-39 of it.  Each value's

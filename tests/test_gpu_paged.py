@@ -540,3 +540,21 @@ def test_bad_pages_and_lengths_without_a_workspace_give_zeros():
     q = torch.ones(4, 4, 128, dtype=BF16, device=DEV)
     out = M.msa_paged_append(k, k, *pages, table, n, cu_new=cu, q=q)
     assert (out[:2] == 1).all() and (out[2:] == 0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_runs_that_start_behind_the_first_hundred_sequences(fp8):
+    """200 sequences, long ones on both sides of the 128 whose tiles are summed
+    at once, empty ones between: runs begin in the second lot and cross it."""
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 40, 200).tolist()
+    for b, n in ((3, 5000), (100, 2100), (126, 3000), (127, 0), (128, 4100), (129, 0), (150, 6000), (198, 900), (199, 0)):
+        lens[b] = n
+    c = make_cache(lens, 2, 16, fp8, seed=53)
+    q = torch.randn(200, 8, 128, generator=torch.Generator().manual_seed(8)).to(BF16).to(DEV)
+    ws = M.new_paged_workspace(M.MSA_OP_PAGED_DECODE, c["table"], 16, 8, 2)
+    out, lse = decode(c, q, lens, ws=ws)
+    check_decode(c, q, lens, out, lse)
+    again, _ = decode(c, q, lens, ws=ws)
+    assert torch.equal(out, again)
+    assert M.msa_read_status(ws) == M.MSA_OK
