@@ -421,3 +421,19 @@ def test_a_refused_batch_without_a_workspace_gives_zeros():
         grads = M.msa_dense_attn_varlen_backward(x["q"], x["k"], x["v"], out, lse, x["dout"], cq, ck)
         assert all((t == 0).all() for t in grads)
         del grads
+
+
+@pytest.mark.parametrize("R", [1, 4, 16])
+@pytest.mark.parametrize("lens_q,lens_k", [([7, 9], [0, 0]), ([0, 0], [7, 9]), ([300], [0]), ([0], [300]),
+                                           ([1] * 40, [0] * 40), ([0] * 40, [200] * 40)])
+def test_no_keys_or_no_queries(lens_q, lens_k, R):
+    """Buffers of no rows at all: results are zero (lse -inf), and written."""
+    x, cq, ck = packed(lens_q, lens_k, 2, R, seed=R, tail=0)
+    ws = M.new_dense_workspace(M.MSA_OP_DENSE_VARLEN, x["q"], x["k"], len(lens_q))
+    out, lse = run(x, cq, ck, ws=ws)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    wsb = M.new_dense_workspace(M.MSA_OP_DENSE_VARLEN_BACKWARD, x["q"], x["k"], len(lens_q))
+    g = {n: torch.full_like(x[n[1:]], 7.0) for n in ("dq", "dk", "dv")}
+    M.msa_dense_attn_varlen_backward(x["q"], x["k"], x["v"], out, lse, x["dout"], i32(cq), i32(ck), ws=wsb, **g)
+    assert all((t == 0).all() for t in g.values())
+    assert M.msa_read_status(ws) == M.MSA_OK and M.msa_read_status(wsb) == M.MSA_OK
