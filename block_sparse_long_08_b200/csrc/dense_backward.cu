@@ -65,15 +65,6 @@ struct RingPos {
 constexpr int kBRegsRest = 72, kBRegsSoftmax = 216;   // 128 * 72 + 256 * 216 = 384 * 168
 constexpr uint32_t kBDescHi = sdesc_hi(1024);
 
-template <uint32_t N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <uint32_t N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // D (+)= A B^T over 128 elements of the head dim, both operands K-major tiles.
 __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a_lo, uint32_t b_lo) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);

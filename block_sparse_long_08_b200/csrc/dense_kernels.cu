@@ -291,15 +291,6 @@ __device__ __forceinline__ bool dense_item(const DenseArgs &a, const FSmall &sm,
   return true;
 }
 
-template <uint32_t N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <uint32_t N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 template <int R>
 __global__ void __launch_bounds__(kFThreads, 1)
     dense_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace msa {
 
@@ -303,11 +304,6 @@ __device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t w, float f) {
 // f16 holds rows of any size (elements down to 2^-28 of the row's largest keep
 // their bits, the others are off by 2^-39 of it).  2^(254 - field - 127) undoes it.
 __device__ __forceinline__ uint32_t f16_lift(float x) { return min(268u - (__float_as_uint(x) >> 23), 239u); }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Byte of 16-byte granule gr of row r in a stage: rows of 256 bytes (8-bit:
 // 128), granules permuted so that eight rows of one granule (8-bit: two
@@ -608,10 +604,10 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > kPdWTop);
         const bool wu1 = y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > kPdWTop);
         if (__any_sync(0xffffffffu, up0 || up1 || wu0 || wu1)) {
-          if (up0) { l0 *= m0 == -INFINITY ? 0.f : exp2_fast(m0 - x0); m0 = x0; }
-          if (up1) { l1 *= m1 == -INFINITY ? 0.f : exp2_fast(m1 - x1); m1 = x1; }
-          const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - (y0 - kPdWRef))) : 1.f;
-          const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - (y1 - kPdWRef))) : 1.f;
+          if (up0) { l0 *= m0 == -INFINITY ? 0.f : fast_exp2(m0 - x0); m0 = x0; }
+          if (up1) { l1 *= m1 == -INFINITY ? 0.f : fast_exp2(m1 - x1); m1 = x1; }
+          const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : fast_exp2(mw0 - (y0 - kPdWRef))) : 1.f;
+          const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : fast_exp2(mw1 - (y1 - kPdWRef))) : 1.f;
           if (wu0) mw0 = y0 - kPdWRef;
           if (wu1) mw1 = y1 - kPdWRef;
 #pragma unroll
@@ -620,13 +616,13 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
             o[d][1] *= al1; o[d][3] *= al1;
           }
         }
-        l0 += exp2_fast(s[0] - m0) + exp2_fast(s[2] - m0);
-        l1 += exp2_fast(s[1] - m1) + exp2_fast(s[3] - m1);
+        l0 += fast_exp2(s[0] - m0) + fast_exp2(s[2] - m0);
+        l1 += fast_exp2(s[1] - m1) + fast_exp2(s[3] - m1);
         const float n0 = mw0 == -INFINITY ? 0.f : -mw0, n1 = mw1 == -INFINITY ? 0.f : -mw1;
-        const __half2 p0 = __floats2half2_rn(copysignf(exp2_fast(s[0] + lv0 + n0), v0),
-                                             copysignf(exp2_fast(s[1] + lv0 + n1), v0));
-        const __half2 p1 = __floats2half2_rn(copysignf(exp2_fast(s[2] + lv1 + n0), v1),
-                                             copysignf(exp2_fast(s[3] + lv1 + n1), v1));
+        const __half2 p0 = __floats2half2_rn(copysignf(fast_exp2(s[0] + lv0 + n0), v0),
+                                             copysignf(fast_exp2(s[1] + lv0 + n1), v0));
+        const __half2 p1 = __floats2half2_rn(copysignf(fast_exp2(s[2] + lv1 + n0), v1),
+                                             copysignf(fast_exp2(s[3] + lv1 + n1), v1));
         const uint32_t b0 = transpose8(*reinterpret_cast<const uint32_t *>(&p0));
         const uint32_t b1 = transpose8(*reinterpret_cast<const uint32_t *>(&p1));
         // O^T += V^T P^T: this lane's dims are 16 g4 .. + 15 (rows g4 and g4 + 8
@@ -726,8 +722,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         const bool up0 = m0 == -INFINITY || (x0 - m0) * unit > 8.f;
         const bool up1 = R > 8 && (m1 == -INFINITY || (x1 - m1) * unit > 8.f);
         if (__any_sync(0xffffffffu, up0 || up1)) {
-          const float al0 = up0 ? (m0 == -INFINITY ? 0.f : exp2_fast((m0 - x0) * unit)) : 1.f;
-          const float al1 = up1 ? (m1 == -INFINITY ? 0.f : exp2_fast((m1 - x1) * unit)) : 1.f;
+          const float al0 = up0 ? (m0 == -INFINITY ? 0.f : fast_exp2((m0 - x0) * unit)) : 1.f;
+          const float al1 = up1 ? (m1 == -INFINITY ? 0.f : fast_exp2((m1 - x1) * unit)) : 1.f;
           if (up0) m0 = x0;
           if (up1) m1 = x1;
           l0 *= al0;
@@ -763,8 +759,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
           const bool wu0 = y0 > -INFINITY && (mw0 == -INFINITY || y0 - mw0 > kPdWTop);
           const bool wu1 = R > 8 && y1 > -INFINITY && (mw1 == -INFINITY || y1 - mw1 > kPdWTop);
           if (__any_sync(0xffffffffu, wu0 || wu1)) {
-            const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : exp2_fast(mw0 - (y0 - kPdWRef))) : 1.f;
-            const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : exp2_fast(mw1 - (y1 - kPdWRef))) : 1.f;
+            const float al0 = wu0 ? (mw0 == -INFINITY ? 0.f : fast_exp2(mw0 - (y0 - kPdWRef))) : 1.f;
+            const float al1 = wu1 ? (mw1 == -INFINITY ? 0.f : fast_exp2(mw1 - (y1 - kPdWRef))) : 1.f;
             if (wu0) mw0 = y0 - kPdWRef;
             if (wu1) mw1 = y1 - kPdWRef;
 #pragma unroll
@@ -782,11 +778,11 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
           for (int h = 0; h < (R > 8 ? 2 : 1); ++h) {   // rows g4, then g4 + 8
             const float z0 = s[i][2 * h] * unit, z1 = s[i][2 * h + 1] * unit;
             const float n = h ? n1 : n0, w = h ? w1 : w0;
-            const float p0 = exp2_fast(z0 + n), p1 = exp2_fast(z1 + n);
+            const float p0 = fast_exp2(z0 + n), p1 = fast_exp2(z1 + n);
             if (h) l1 += p0 + p1; else l0 += p0 + p1;
             if (FP8) {
-              const __half2 x = __floats2half2_rn(copysignf(exp2_fast(z0 + lv[i][0] + w), vs[i][0]),
-                                                  copysignf(exp2_fast(z1 + lv[i][1] + w), vs[i][1]));
+              const __half2 x = __floats2half2_rn(copysignf(fast_exp2(z0 + lv[i][0] + w), vs[i][0]),
+                                                  copysignf(fast_exp2(z1 + lv[i][1] + w), vs[i][1]));
               pa[2 * i + h] = *reinterpret_cast<const uint32_t *>(&x);
             } else {
               pa[2 * i + h] = pack_bf16x2(p0, p1);
@@ -840,8 +836,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         }
         // O's unit, 2^(scale m) (8-bit: 2^mw), to 2^(scale M)
         const float unit0 = FP8 ? mw0 : m0 * a.scale_log2, unit1 = FP8 ? mw1 : m1 * a.scale_log2;
-        const float f0 = unit0 == -INFINITY ? 0.f : exp2_fast(unit0 - M0 * a.scale_log2);
-        const float f1 = unit1 == -INFINITY ? 0.f : exp2_fast(unit1 - M1 * a.scale_log2);
+        const float f0 = unit0 == -INFINITY ? 0.f : fast_exp2(unit0 - M0 * a.scale_log2);
+        const float f1 = unit1 == -INFINITY ? 0.f : fast_exp2(unit1 - M1 * a.scale_log2);
         // warp by warp, so that the sum's order is always the same
         for (int w = 0; w < 4; ++w) {
           if (C::KM && w == warp) {
@@ -884,7 +880,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
           for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w * 16 + r]);
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            L += s_m[w * 16 + r] == -INFINITY ? 0.f : s_l[w * 16 + r] * exp2_fast((s_m[w * 16 + r] - M) * a.scale_log2);
+            L += s_m[w * 16 + r] == -INFINITY ? 0.f : s_l[w * 16 + r] * fast_exp2((s_m[w * 16 + r] - M) * a.scale_log2);
           const float x = s_o[r * kHeadDim + tid];
           if (CL) {
             if (tid == 0) s_part[r] = make_float2(M, L);
@@ -934,7 +930,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
       for (int p = 0; p < 8; ++p) M = fmaxf(M, m[p]);
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
-        const float f = m[p] == -INFINITY ? 0.f : exp2_fast((m[p] - M) * a.scale_log2);
+        const float f = m[p] == -INFINITY ? 0.f : fast_exp2((m[p] - M) * a.scale_log2);
         L = fmaf(f, l[p], L);
         O = m[p] == -INFINITY ? O : fmaf(f, x[p], O);   // (a CTA without tiles left x unwritten)
       }
@@ -988,7 +984,7 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const PagedDecodeArgs a
   for (int p = grp; p < n; p += 4) {
     const float *q = part(p);
     const float mp = __ldcg(q + kHeadDim), lp = __ldcg(q + kHeadDim + 1), op = __ldcg(q + d);
-    const float f = mp == -INFINITY ? 0.f : exp2_fast((mp - M) * a.scale_log2);
+    const float f = mp == -INFINITY ? 0.f : fast_exp2((mp - M) * a.scale_log2);
     x = fmaf(f, op, x);
     l = fmaf(f, lp, l);
   }
