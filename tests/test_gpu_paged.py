@@ -558,3 +558,20 @@ def test_decode_runs_that_start_behind_the_first_hundred_sequences(fp8):
     again, _ = decode(c, q, lens, ws=ws)
     assert torch.equal(out, again)
     assert M.msa_read_status(ws) == M.MSA_OK
+
+
+@pytest.mark.parametrize("lens,G,R,cols", [([300, 33, 1], 2, 4, 20), ([300, 33, 2], 1, 16, 20), ([9000, 700], 2, 8, 600),
+                                           ([9000, 700], 1, 16, 600), ([5000], 1, 1, 400)])
+def test_decode_bf16_rounds_nothing_but_its_results(lens, G, R, cols):
+    """The weights enter their product in two bf16 terms, so what they lose is
+    a rounding of a rounding's rest, 2^-16 of them; the result is rounded once."""
+    c = make_cache(lens, G, 16, False, seed=54, cols=cols)
+    q = torch.randn(len(lens), G * R, 128, generator=torch.Generator().manual_seed(9)).to(BF16).to(DEV)
+    out = f64(decode(c, q, lens)[0])
+    for b, n in enumerate(lens):
+        k, v = gathered(c, "k", b, n), gathered(c, "v", b, n)
+        for h in range(G * R):
+            ref, _, p, _, dz = O.attend(f64(q[b, h])[None], k[:, h // R], v[:, h // R], 128 ** -0.5, [n])
+            tol = O.U * np.abs(ref) + (2.0 ** -16 + 2 * (dz + 2.0 ** -20))[:, None] * (p @ np.abs(v[:, h // R]))
+            err = np.abs(out[b, h] - ref[0])
+            assert (err <= tol[0]).all(), (b, h, (err - tol[0]).max())
