@@ -575,3 +575,20 @@ def test_decode_bf16_rounds_nothing_but_its_results(lens, G, R, cols):
             tol = O.U * np.abs(ref) + (2.0 ** -16 + 2 * (dz + 2.0 ** -20))[:, None] * (p @ np.abs(v[:, h // R]))
             err = np.abs(out[b, h] - ref[0])
             assert (err <= tol[0]).all(), (b, h, (err - tol[0]).max())
+
+
+@pytest.mark.parametrize("cols", [60, 300])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("R", [1, 4, 16])
+def test_decode_nan_in_a_query_stays_with_its_head(R, fp8, cols):
+    lens = [40, 900, 7]
+    c = make_cache(lens, 2, 16, fp8, seed=55, cols=cols)
+    q = torch.randn(3, 2 * R, 128, generator=torch.Generator().manual_seed(4)).to(BF16).to(DEV)
+    out, lse = decode(c, q, lens)
+    hit = torch.zeros(3, 2 * R, dtype=torch.bool, device=DEV)
+    for b, h, d, x in ((0, R, 5, "nan"), (1, 0, 127, "nan"), (2, 2 * R - 1, 64, "inf")):
+        q[b, h, d] = float(x)
+        hit[b, h] = True
+    o, ls = decode(c, q, lens)
+    assert torch.isnan(o[hit][:2]).all() and torch.isnan(ls[hit][:2]).all()
+    assert torch.equal(o[~hit], out[~hit]) and torch.equal(ls[~hit], lse[~hit])
