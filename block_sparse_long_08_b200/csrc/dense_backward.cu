@@ -18,14 +18,20 @@
 // result repeats bit for bit) and nothing of dq's size is kept in fp32.
 // P and dZ are rounded to bf16 for their products (Q, K and dO are bf16, and
 // both operands of a UMMA have one type).  Every element's rounding is its own,
-// of the size of the results' last one: dq and dk are 2.5e-3 of their norm off
-// where a single rounding at the end gives 1.7e-3, dv 2.3e-3.  D comes from
-// out as bf16, as the caller holds it.
+// of the size of the results' last one: with random rows of 1000 keys and more
+// dq and dk are 2.4e-3 of their norm off where a single rounding at the end
+// gives 1.7e-3, dv 2.3e-3.  D is an fp32 sum over out as bf16, as the caller
+// holds it, and what that rounding costs does not shrink where dP and D nearly
+// cancel: dq and dk are 3.5e-3 off for sequences of two tokens, 3.0e-3 of
+// eight, and 3.7e-3 (5.2e-3) for 1000 tokens whose queries are four (eight)
+// times as large.
 // Measured: 8192 tokens, 32 heads on 8, 1.34 ms from idle (7 products of 128^3
 // per tile pair; 1026 TFLOP/s, 0.62 of burst bf16, over the 5 counted); 7.3K tokens in seven
-// documents, 16 heads on 4, 136-158 us.  A step of dkv takes 2680 cycles for
-// 2050 of products, one of dq 2020 for 1540: the softmax's chain (exponentials
-// 1030 of the MUFU unit, loads and stores of TMEM around them) bounds both.
+// documents, 16 heads on 4, 136-158 us.  Over that whole 8192-token call, items'
+// starts and ends among them, a tile pair takes dkv 2860 cycles for 2048 of
+// products (four of 512) and dq 2130 for 1536; in the steady state (read with
+// clock()) 2560 and 1880.  The softmax's chain (exponentials 1024 of the MUFU
+// unit, loads and stores of TMEM around them) bounds both.
 // Tried and not faster: exponentials as polynomials on the FMA pipe, K and V
 // (Q and dO) released before the last product, dq stored under the next item's
 // first products, halves of a dq tile skipped where no row sees them.
@@ -160,7 +166,7 @@ constexpr uint32_t kVTmS = 0, kVTmDP = 128, kVTmDV = 256, kVTmDK = 384;
 // dZ once it has read them), so the order of the UMMAs is
 //   dV += P_i dO_i | dK += dZ_i Q_i, dP_i+1, S_i+2
 // (the bar: behind P_i, behind dZ_i) and the exponentials of tile i+1 run
-// under all of it: about 2000 cycles of softmax over 2240 of products.
+// under all of it.
 template <int R>
 __global__ void __launch_bounds__(kBThreads, 1)
     dense_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
