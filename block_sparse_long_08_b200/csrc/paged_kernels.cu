@@ -849,11 +849,11 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<R, FP8>::CTAS)) paged_decod
         const float unit0 = FP8 ? mw0 : m0 * a.scale_log2, unit1 = FP8 ? mw1 : m1 * a.scale_log2;
         const float f0 = unit0 == -INFINITY ? 0.f : fast_exp2(unit0 - M0 * a.scale_log2);
         const float f1 = unit1 == -INFINITY ? 0.f : fast_exp2(unit1 - M1 * a.scale_log2);
-        if (!FP8 && R <= 8) {   // the products of P's two terms
+        if (!FP8 && R <= 8) {   // the products of P's two terms (an infinite value's second one is NaN)
 #pragma unroll
           for (int d = 0; d < 16; ++d) {
-            o[d][0] += o[d][2];
-            o[d][1] += o[d][3];
+            o[d][0] = fabsf(o[d][0]) == INFINITY ? o[d][0] : o[d][0] + o[d][2];
+            o[d][1] = fabsf(o[d][1]) == INFINITY ? o[d][1] : o[d][1] + o[d][3];
           }
         }
         // warp by warp, so that the sum's order is always the same

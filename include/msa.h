@@ -477,9 +477,10 @@ int msa_paged_append(const msa_params *p, const msa_paged_cache *c, int n_rows, 
  *   out [B,H,d] bf16; lse [B,H] fp32 or NULL                            (out)
  * Cache rows at and behind seq_lens[b] may hold anything; a NaN in a query or
  * an attended row makes that head's out (a key's: its lse too) NaN, and
- * nothing else.  seq_lens[b]
- * outside [0, p->L] sets MSA_ERR_DEVICE_INPUT (out 0, lse -inf); the keys of
- * a page whose id lies outside [0, num_pages) are left out and set it too.
+ * nothing else; an infinite attended value makes that dim of its heads
+ * infinite or NaN, and nothing else.  seq_lens[b] outside [0, p->L] sets
+ * MSA_ERR_DEVICE_INPUT (out 0, lse -inf); the keys of a page whose id lies
+ * outside [0, num_pages) are left out and set it too.
  * The cache's tokens are shared out over the SMs whatever the lengths, the
  * parts of one sequence joined by a second launch (short calls: within one);
  * the split depends on the lengths, p and the device's number of SMs alone,

@@ -592,3 +592,22 @@ def test_decode_nan_in_a_query_stays_with_its_head(R, fp8, cols):
     o, ls = decode(c, q, lens)
     assert torch.isnan(o[hit][:2]).all() and torch.isnan(ls[hit][:2]).all()
     assert torch.equal(o[~hit], out[~hit]) and torch.equal(ls[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("cols", [60, 300])
+@pytest.mark.parametrize("R", [1, 4, 8, 16])
+def test_decode_infinite_value_stays_in_its_dim(R, cols):
+    lens = [40, 900, 7]
+    c = make_cache(lens, 2, 16, False, seed=56, cols=cols)
+    q = torch.randn(3, 2 * R, 128, generator=torch.Generator().manual_seed(4)).to(BF16).to(DEV)
+    out, lse = decode(c, q, lens)
+    for b, t, g, d, x in ((0, 17, 1, 5, "inf"), (1, 899, 0, 127, "-inf")):
+        c["v"][c["table"][b, t // 16].long(), t % 16, g, d] = float(x)
+    o, ls = decode(c, q, lens)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, R:, 5], hit[1, :R, 127] = True, True
+    assert torch.equal(o[~hit], out[~hit]) and torch.equal(ls, lse)
+    if R <= 8:
+        assert (o[0, R:, 5] == float("inf")).all() and (o[1, :R, 127] == -float("inf")).all()
+    else:
+        assert not torch.isfinite(o[hit]).any()
